@@ -25,7 +25,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 KVQ_OK, KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED, KVQ_ERR_CAPACITY, KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA, KVQ_ERR_DEVICE = range(7)
 KVQ_DECODE_STATIC_SCRATCH_BYTES = 16 << 20  # size of the fixed scratch of kvq_decode_attention_static
-KVQ_DEV_BAD_PAGE, KVQ_DEV_OVERFLOW, KVQ_DEV_BAD_SET, KVQ_DEV_TIMEOUT, KVQ_DEV_RANGE = 0x1, 0x2, 0x4, 0x8, 0x10
+KVQ_DEV_BAD_PAGE, KVQ_DEV_OVERFLOW, KVQ_DEV_BAD_SET, KVQ_DEV_TIMEOUT, KVQ_DEV_RANGE, KVQ_DEV_NO_PAGES = 0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 KVQ_F16, KVQ_BF16 = 0, 1
 KVQ_TX_NONE, KVQ_TX_HADAMARD_VARNORM = 0, 1
 HEAD_DIM, GROUP = 128, 32
@@ -52,7 +52,16 @@ class kvq_cache(ctypes.Structure):
     ]
 
 
+class kvq_rows(ctypes.Structure):
+    _fields_ = [
+        ("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("heads", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("in_tok_stride", ctypes.c_int64), ("in_head_stride", ctypes.c_int64),
+        ("out_tok_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+    ]
+
+
 _P = ctypes.POINTER(kvq_cache)
+_R = ctypes.POINTER(kvq_rows)
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _SIGS = {
     "kvq_page_bytes": (_sz, [_P]),
@@ -68,6 +77,14 @@ _SIGS = {
     "kvq_decode_attention_static": (ctypes.c_int, [_P, _vp, _i32, _f32, _vp, _vp]),
     "kvq_step_workspace_bytes": (_sz, [_P, _i32]),
     "kvq_decode_step": (ctypes.c_int, [_P, _vp, _vp, _vp, _i32, _f32, _vp, _vp, _sz, _vp]),
+    "kvq_norm_rope": (ctypes.c_int, [_R, _R, _R, _i32, _i64, _vp, _vp, _i32, _i32, _f32, _vp]),
+    "kvq_plan_workspace_bytes": (_sz, [_P]),
+    "kvq_plan_pages": (ctypes.c_int, [_P, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "kvq_page_bounds": (ctypes.c_int, [_P, _vp, _i32, _vp, _vp]),
+    "kvq_select_workspace_bytes": (_sz, [_P]),
+    "kvq_select_pages": (ctypes.c_int, [_P, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "kvq_decode_pages_workspace_bytes": (_sz, [_P, _i32, _i32]),
+    "kvq_decode_attention_pages": (ctypes.c_int, [_P, _vp, _i32, _f32, _vp, _vp, _i32, _vp, _vp, _sz, _vp]),
     "kvq_dequantize": (ctypes.c_int, [_P, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
     "kvq_read_status": (ctypes.c_int, [_P, ctypes.POINTER(_i32), _i32, _vp]),
     "kvq_mine_read_status": (ctypes.c_int, [_vp, ctypes.POINTER(_i32), _vp]),
@@ -178,6 +195,143 @@ def kvq_decode_step(cache: kvq_cache, k_new: torch.Tensor, v_new: torch.Tensor, 
     """One-token quantize-append + decode attention in one launch (workspace zero-filled before first use)."""
     _check(_lib.kvq_decode_step(ctypes.byref(cache), _ptr(k_new), _ptr(v_new), _ptr(q), num_q_heads, sm_scale,
                                 _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# The rest of a serving step: rows, pages, bounds, selection, attention over chosen pages.
+# These wrappers check what the C side cannot see (element types, shapes, devices).
+# ---------------------------------------------------------------------------
+
+_TORCH_DT = {KVQ_F16: torch.float16, KVQ_BF16: torch.bfloat16}
+
+
+def _want(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple | None = None) -> None:
+    """A CUDA tensor of the current device, of this type and (unless None) contiguous in this shape."""
+    if t.dtype != dtype:
+        raise KvqError(KVQ_ERR_INVALID_ARG, f"{name} is {t.dtype}, not {dtype}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise KvqError(KVQ_ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current CUDA device")
+    if shape is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
+        raise KvqError(KVQ_ERR_INVALID_ARG, f"{name} must be contiguous {list(shape)}, got {list(t.shape)} with strides {list(t.stride())}")
+
+
+def _ws_bytes(ws: torch.Tensor | None) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def _rows(name: str, x: torch.Tensor | None, out: torch.Tensor | None, weight: torch.Tensor | None, dtype, tokens: int) -> kvq_rows:
+    r = kvq_rows()
+    if x is None:
+        return r
+    if out is None:
+        raise KvqError(KVQ_ERR_INVALID_ARG, f"{name} has no output")
+    for label, t in ((name, x), (name + "_out", out)):
+        _want(label, t, dtype)
+        if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != x.shape[1] or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
+            raise KvqError(KVQ_ERR_INVALID_ARG, f"{label} must be [{tokens}, heads, {HEAD_DIM}] with contiguous rows, got {list(t.shape)} "
+                           f"with strides {list(t.stride())}")
+    if weight is not None:
+        _want(name + "_weight", weight, dtype, (HEAD_DIM,))
+        r.weight = weight.data_ptr()
+    r.in_, r.out, r.heads = x.data_ptr(), out.data_ptr(), x.shape[1]
+    # a dimension of one element has a stride nobody reads: whatever it says, it is none
+    r.in_tok_stride, r.in_head_stride = (x.stride(i) if x.shape[i] > 1 else 0 for i in (0, 1))
+    r.out_tok_stride, r.out_head_stride = (out.stride(i) if out.shape[i] > 1 else 0 for i in (0, 1))
+    return r
+
+
+def kvq_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None, positions: torch.Tensor | None,
+                  inv_freq: torch.Tensor | None, q_out: torch.Tensor | None, k_out: torch.Tensor | None,
+                  v_out: torch.Tensor | None, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                  eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """Per-head RMS norm (where a weight is given) and rotation of q and k, and v copied, in one pass.
+
+    q, k, v and their outputs are [tokens, heads, 128] of one 16-bit type; token and head strides are free (slices of a
+    packed projection), rows contiguous.  Any of q, k, v may be None.  positions [tokens] int32; inv_freq [rot_dim / 2]
+    fp32, whose length sets rot_dim (None: no rotation)."""
+    given = [t for t in (q, k, v) if t is not None]
+    if not given:
+        return
+    dtype, tokens = given[0].dtype, given[0].shape[0]
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise KvqError(KVQ_ERR_UNSUPPORTED, f"rows of {dtype}")
+    rq = _rows("q", q, q_out, q_weight, dtype, tokens)
+    rk = _rows("k", k, k_out, k_weight, dtype, tokens)
+    rv = _rows("v", v, v_out, None, dtype, tokens)
+    rot = 0
+    if inv_freq is not None and inv_freq.numel():
+        _want("inv_freq", inv_freq, torch.float32, (inv_freq.numel(),))
+        rot = 2 * inv_freq.numel()
+        if q is not None or k is not None:
+            if positions is None:
+                raise KvqError(KVQ_ERR_INVALID_ARG, "a rotation needs positions")
+            _want("positions", positions, torch.int32, (tokens,))
+    _check(_lib.kvq_norm_rope(ctypes.byref(rq), ctypes.byref(rk), ctypes.byref(rv),
+                              KVQ_BF16 if dtype == torch.bfloat16 else KVQ_F16, tokens, _ptr(positions), _ptr(inv_freq), rot,
+                              int(interleaved), eps, _stream(stream)))
+
+
+def kvq_plan_workspace_bytes(cache: kvq_cache) -> int:
+    return int(_lib.kvq_plan_workspace_bytes(ctypes.byref(cache)))
+
+
+def kvq_plan_pages(cache: kvq_cache, new_len: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+                   free_left: torch.Tensor, cu_new: torch.Tensor, slot_map: torch.Tensor, positions: torch.Tensor,
+                   seq_ids: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """Page tables, slot map and positions of a batch from its request lengths (include/kvq.h)."""
+    i32, n = torch.int32, slot_map.numel()
+    _want("new_len", new_len, i32, (cache.num_seqs,))
+    _want("free_pages", free_pages, i32, (free_pages.numel(),))
+    _want("free_count", free_count, i32, (1,))
+    _want("free_left", free_left, i32, (1,))
+    _want("cu_new", cu_new, i32, (cache.num_seqs + 1,))
+    _want("slot_map", slot_map, torch.int64, (n,))
+    _want("positions", positions, i32, (n,))
+    _want("seq_ids", seq_ids, i32, (n,))
+    _check(_lib.kvq_plan_pages(ctypes.byref(cache), _ptr(new_len), _ptr(free_pages), free_pages.numel(), _ptr(free_count),
+                               _ptr(free_left), _ptr(cu_new), _ptr(slot_map), _ptr(positions), _ptr(seq_ids), n, _ptr(ws),
+                               _ws_bytes(ws), _stream(stream)))
+
+
+def kvq_page_bounds(cache: kvq_cache, k_new: torch.Tensor, n_new: int, bounds: torch.Tensor, stream=None) -> None:
+    """Minimum and maximum of the keys per page and channel, with the keys of an append, before it."""
+    dt = _TORCH_DT.get(cache.dtype)
+    _want("k_new", k_new, dt, (cache.num_seqs, n_new, cache.num_kv_heads, HEAD_DIM))
+    _want("bounds", bounds, dt, (cache.num_pages, cache.num_kv_heads, 2, HEAD_DIM))
+    _check(_lib.kvq_page_bounds(ctypes.byref(cache), _ptr(k_new), n_new, _ptr(bounds), _stream(stream)))
+
+
+def kvq_select_workspace_bytes(cache: kvq_cache) -> int:
+    return int(_lib.kvq_select_workspace_bytes(ctypes.byref(cache)))
+
+
+def kvq_select_pages(cache: kvq_cache, q: torch.Tensor, num_q_heads: int, bounds: torch.Tensor, budget: int, sink: int,
+                     recent: int, page_list: torch.Tensor, list_len: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """The pages each (sequence, KV head) attends to, by an upper bound of its scores (workspace zero-filled before first use)."""
+    dt, B, H = _TORCH_DT.get(cache.dtype), cache.num_seqs, cache.num_kv_heads
+    _want("q", q, dt, (B, num_q_heads, HEAD_DIM))
+    _want("bounds", bounds, dt, (cache.num_pages, H, 2, HEAD_DIM))
+    _want("page_list", page_list, torch.int32, (B, H, budget))
+    _want("list_len", list_len, torch.int32, (B, H))
+    _check(_lib.kvq_select_pages(ctypes.byref(cache), _ptr(q), num_q_heads, _ptr(bounds), budget, sink, recent, _ptr(page_list),
+                                 _ptr(list_len), _ptr(ws), _ws_bytes(ws), _stream(stream)))
+
+
+def kvq_decode_pages_workspace_bytes(cache: kvq_cache, num_q_heads: int, budget: int) -> int:
+    return int(_lib.kvq_decode_pages_workspace_bytes(ctypes.byref(cache), num_q_heads, budget))
+
+
+def kvq_decode_attention_pages(cache: kvq_cache, q: torch.Tensor, num_q_heads: int, sm_scale: float, page_list: torch.Tensor,
+                               list_len: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """kvq_decode_attention over listed pages only; `out` is in the cache's dtype (workspace zero-filled before first use)."""
+    dt, B, H = _TORCH_DT.get(cache.dtype), cache.num_seqs, cache.num_kv_heads
+    budget = page_list.shape[-1]
+    _want("q", q, dt, (B, num_q_heads, HEAD_DIM))
+    _want("out", out, dt, (B, num_q_heads, HEAD_DIM))
+    _want("page_list", page_list, torch.int32, (B, H, budget))
+    _want("list_len", list_len, torch.int32, (B, H))
+    _check(_lib.kvq_decode_attention_pages(ctypes.byref(cache), _ptr(q), num_q_heads, sm_scale, _ptr(page_list), _ptr(list_len),
+                                           budget, _ptr(out), _ptr(ws), _ws_bytes(ws), _stream(stream)))
 
 
 def kvq_dequantize(cache: kvq_cache, seq: int, seq_len_host: int, start: int, count: int,
@@ -310,6 +464,41 @@ class PagedKVCache:
         """kvq_decode_step: k_new / v_new [num_seqs][num_kv_heads][128], q [num_seqs][num_q_heads][128]."""
         scale = HEAD_DIM ** -0.5 if sm_scale is None else sm_scale
         kvq_decode_step(self.c, k_new, v_new, q, int(q.shape[1]), scale, out, ws, stream)
+
+    # -- the rest of a serving step ------------------------------------------------------------
+
+    def plan_workspace(self) -> torch.Tensor:
+        return _alloc_aligned(max(256, kvq_plan_workspace_bytes(self.c)), self.device)
+
+    def plan(self, new_len: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor, cu_new: torch.Tensor,
+             slot_map: torch.Tensor, positions: torch.Tensor, seq_ids: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+        """kvq_plan_pages: page_table takes the new pages, popped off the stack (free_pages, free_count)."""
+        kvq_plan_pages(self.c, new_len, free_pages, free_count, free_count, cu_new, slot_map, positions, seq_ids, ws, stream)
+
+    def bounds(self) -> torch.Tensor:
+        """Buffer of kvq_page_bounds / kvq_select_pages: [num_pages][num_kv_heads][2][128] in the cache's dtype."""
+        return torch.zeros(self.num_pages, self.H, 2, HEAD_DIM, dtype=_TORCH_DT[self.dtype], device=self.device)
+
+    def update_bounds(self, k_new: torch.Tensor, bounds: torch.Tensor, stream=None) -> None:
+        """kvq_page_bounds with the keys of an append [num_seqs][n_new][num_kv_heads][128], before it."""
+        kvq_page_bounds(self.c, k_new, int(k_new.shape[1]), bounds, stream)
+
+    def select_workspace(self) -> torch.Tensor:
+        return _alloc_aligned(max(256, kvq_select_workspace_bytes(self.c)), self.device, zero=True)
+
+    def select(self, q: torch.Tensor, bounds: torch.Tensor, page_list: torch.Tensor, list_len: torch.Tensor, ws: torch.Tensor,
+               sink: int = 1, recent: int = 2, stream=None) -> None:
+        """kvq_select_pages into page_list [num_seqs][num_kv_heads][budget] and list_len [num_seqs][num_kv_heads]."""
+        kvq_select_pages(self.c, q, int(q.shape[1]), bounds, int(page_list.shape[-1]), sink, recent, page_list, list_len, ws, stream)
+
+    def decode_pages_workspace(self, num_q_heads: int, budget: int) -> torch.Tensor:
+        return _alloc_aligned(max(256, kvq_decode_pages_workspace_bytes(self.c, num_q_heads, budget)), self.device, zero=True)
+
+    def decode_pages(self, q: torch.Tensor, page_list: torch.Tensor, list_len: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+                     sm_scale: float | None = None, stream=None) -> None:
+        """kvq_decode_attention_pages; out [num_seqs][num_q_heads][128] in the cache's dtype."""
+        scale = HEAD_DIM ** -0.5 if sm_scale is None else sm_scale
+        kvq_decode_attention_pages(self.c, q, int(q.shape[1]), scale, page_list, list_len, out, ws, stream)
 
     def read_status(self, clear: bool = False) -> int:
         return kvq_read_status(self.c, clear)

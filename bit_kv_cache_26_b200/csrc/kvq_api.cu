@@ -237,6 +237,183 @@ kvq_status kvq_decode_step(const kvq_cache* cache, const void* k_new, const void
   return KVQ_OK;
 }
 
+kvq_status kvq_norm_rope(const kvq_rows* q, const kvq_rows* k, const kvq_rows* v, int32_t dtype, int64_t num_tokens,
+                         const int32_t* positions, const float* inv_freq, int32_t rot_dim, int32_t interleaved,
+                         float eps, kvq_stream_t stream) {
+  g_err[0] = 0;
+  if (dtype != KVQ_F16 && dtype != KVQ_BF16) return fail(KVQ_ERR_UNSUPPORTED, "dtype %d", dtype);
+  if (rot_dim < 0 || rot_dim > 128 || rot_dim % 16)
+    return fail(KVQ_ERR_UNSUPPORTED, "rot_dim %d is not a multiple of 16 in 0..128", rot_dim);
+  if (num_tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "num_tokens %lld < 0", (long long)num_tokens);
+  if (num_tokens > INT32_MAX) return fail(KVQ_ERR_CAPACITY, "num_tokens %lld exceeds the launch grid", (long long)num_tokens);
+  if (!(eps >= 0.0f)) return fail(KVQ_ERR_INVALID_ARG, "eps must be >= 0");
+  const kvq_rows* rows[3] = {q, k, v};
+  kvq::RopeArgs a{};
+  int64_t heads = 0;
+  for (int i = 0; i < 3; ++i) {
+    const kvq_rows* r = rows[i];
+    if (!r || r->heads == 0) continue;
+    if (r->reserved != 0) return fail(KVQ_ERR_INVALID_ARG, "reserved field must be 0");
+    if (r->heads < 0) return fail(KVQ_ERR_INVALID_ARG, "negative head count %d", r->heads);
+    heads += r->heads;
+    if (num_tokens == 0) continue;
+    if (!r->in || !r->out) return fail(KVQ_ERR_INVALID_ARG, "rows without an in or out pointer");
+    if (!aligned(r->in, 16) || !aligned(r->out, 16) || (r->weight && !aligned(r->weight, 16)))
+      return fail(KVQ_ERR_INVALID_ARG, "rows and weights must be 16-byte aligned");
+    if (r->in_tok_stride % 8 || r->in_head_stride % 8 || r->out_tok_stride % 8 || r->out_head_stride % 8 ||
+        r->in_tok_stride < 0 || r->in_head_stride < 0 || r->out_tok_stride < 0 || r->out_head_stride < 0)
+      return fail(KVQ_ERR_INVALID_ARG, "strides must be multiples of 8 elements, not negative");
+    if (i == 2 && r->weight) return fail(KVQ_ERR_INVALID_ARG, "values take no weight");
+    a.rows[i] = {r->in, r->out, r->weight, r->heads, r->in_tok_stride, r->in_head_stride, r->out_tok_stride,
+                 r->out_head_stride};
+  }
+  if (num_tokens == 0 || heads == 0) return KVQ_OK;
+  if (heads > 65535) return fail(KVQ_ERR_CAPACITY, "%lld heads in all exceed 65535", (long long)heads);
+  const bool turned = a.rows[0].heads + a.rows[1].heads > 0 && rot_dim > 0;
+  if (turned && (!positions || !inv_freq)) return fail(KVQ_ERR_INVALID_ARG, "positions / inv_freq is NULL");
+  a.pos = positions;
+  a.inv_freq = inv_freq;
+  a.tokens = num_tokens;
+  a.rot = turned ? rot_dim : 0;
+  a.eps = eps;
+  cudaError_t e = kvq::launch_norm_rope(a, dtype, interleaved != 0, num_sms(), (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_norm_rope");
+  return KVQ_OK;
+}
+
+size_t kvq_plan_workspace_bytes(const kvq_cache* cache) {
+  if (!cache || cache->num_seqs < 0) return 0;
+  return kvq::plan_workspace(kvq::make_geom(*cache));
+}
+
+kvq_status kvq_plan_pages(const kvq_cache* cache, const int32_t* new_len, const int32_t* free_pages,
+                          int32_t free_capacity, const int32_t* free_count, int32_t* free_left, int32_t* cu_new,
+                          int64_t* slot_map, int32_t* positions, int32_t* seq_ids, int64_t max_tokens, void* ws,
+                          size_t ws_bytes, kvq_stream_t stream) {
+  g_err[0] = 0;
+  kvq_status s = check_cache(cache);
+  if (s != KVQ_OK) return s;
+  if (cache->num_seqs == 0) return KVQ_OK;
+  if (free_capacity < 0 || max_tokens < 0)
+    return fail(KVQ_ERR_INVALID_ARG, "negative size (free_capacity %d max_tokens %lld)", free_capacity,
+                (long long)max_tokens);
+  if (max_tokens > INT32_MAX - 8192) return fail(KVQ_ERR_CAPACITY, "max_tokens %lld exceeds 2^31 - 8192", (long long)max_tokens);
+  if (!new_len || !free_count || !free_left || !cu_new || (free_capacity > 0 && !free_pages) ||
+      (max_tokens > 0 && (!slot_map || !positions || !seq_ids)))
+    return fail(KVQ_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(slot_map, 16) || !aligned(positions, 16) || !aligned(seq_ids, 16))
+    return fail(KVQ_ERR_INVALID_ARG, "slot_map / positions / seq_ids must be 16-byte aligned");
+  kvq::Geom g = kvq::make_geom(*cache);
+  const size_t need = kvq::plan_workspace(g);
+  if (ws_bytes < need || !ws) return fail(KVQ_ERR_WORKSPACE, "plan workspace %zu < %zu bytes", ws_bytes, need);
+  if (!aligned(ws, 4)) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 4-byte aligned");
+  kvq::PlanArgs a{new_len,  free_pages, free_capacity, free_count, free_left, cu_new,
+                  slot_map, positions,  seq_ids,       max_tokens, (int32_t*)ws};
+  cudaError_t e = kvq::launch_plan(g, a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_plan_pages");
+  return KVQ_OK;
+}
+
+kvq_status kvq_page_bounds(const kvq_cache* cache, const void* k_new, int32_t n_new, void* bounds,
+                           kvq_stream_t stream) {
+  g_err[0] = 0;
+  kvq_status s = check_cache(cache);
+  if (s != KVQ_OK) return s;
+  if (n_new < 0) return fail(KVQ_ERR_INVALID_ARG, "n_new %d < 0", n_new);
+  if (n_new == 0 || cache->num_seqs == 0) return KVQ_OK;
+  if ((int64_t)n_new > (int64_t)cache->max_pages_per_seq * 32)
+    return fail(KVQ_ERR_CAPACITY, "n_new %d exceeds the page table capacity %lld", n_new,
+                (long long)cache->max_pages_per_seq * 32);
+  if (!k_new || !bounds) return fail(KVQ_ERR_INVALID_ARG, "k_new / bounds is NULL");
+  if (!aligned(k_new, 16) || !aligned(bounds, 16))
+    return fail(KVQ_ERR_INVALID_ARG, "k_new / bounds must be 16-byte aligned");
+  cudaError_t e = kvq::launch_page_bounds(kvq::make_geom(*cache), k_new, n_new, bounds, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_page_bounds");
+  return KVQ_OK;
+}
+
+static kvq_status check_q_heads(const kvq_cache* cache, int32_t num_q_heads) {
+  if (num_q_heads < 1 || num_q_heads % cache->num_kv_heads)
+    return fail(KVQ_ERR_UNSUPPORTED, "num_q_heads %d is not a multiple of num_kv_heads %d", num_q_heads,
+                cache->num_kv_heads);
+  if (num_q_heads / cache->num_kv_heads > 16)
+    return fail(KVQ_ERR_UNSUPPORTED, "more than 16 query heads per KV head");
+  return KVQ_OK;
+}
+
+size_t kvq_select_workspace_bytes(const kvq_cache* cache) {
+  if (!cache || cache->num_seqs < 0 || cache->num_kv_heads < 1 || cache->max_pages_per_seq < 0) return 0;
+  return kvq::select_workspace(kvq::make_geom(*cache));
+}
+
+kvq_status kvq_select_pages(const kvq_cache* cache, const void* q, int32_t num_q_heads, const void* bounds,
+                            int32_t budget, int32_t sink, int32_t recent, int32_t* page_list, int32_t* list_len,
+                            void* ws, size_t ws_bytes, kvq_stream_t stream) {
+  g_err[0] = 0;
+  kvq_status s = check_cache(cache);
+  if (s == KVQ_OK) s = check_q_heads(cache, num_q_heads);
+  if (s != KVQ_OK) return s;
+  if (sink < 0 || recent < 1 || (int64_t)sink + recent > budget)
+    return fail(KVQ_ERR_INVALID_ARG, "budget %d, sink %d, recent %d: needs sink >= 0, recent >= 1, sink + recent <= budget",
+                budget, sink, recent);
+  if (cache->num_seqs == 0) return KVQ_OK;
+  if (!q || !bounds || !page_list || !list_len) return fail(KVQ_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(q, 16) || !aligned(bounds, 16)) return fail(KVQ_ERR_INVALID_ARG, "q / bounds must be 16-byte aligned");
+  kvq::Geom g = kvq::make_geom(*cache);
+  const size_t need = kvq::select_workspace(g);
+  if (ws_bytes < need || !ws) return fail(KVQ_ERR_WORKSPACE, "select workspace %zu < %zu bytes", ws_bytes, need);
+  if (!aligned(ws, 256)) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  kvq::SelectArgs a{};
+  a.q = (const uint16_t*)q;
+  a.Gq = num_q_heads / cache->num_kv_heads;
+  a.bounds = (const uint16_t*)bounds;
+  a.budget = budget;
+  a.sink = sink;
+  a.recent = recent;
+  a.list = page_list;
+  a.list_len = list_len;
+  cudaError_t e = kvq::launch_select(g, a, ws, num_sms(), (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_select_pages");
+  return KVQ_OK;
+}
+
+size_t kvq_decode_pages_workspace_bytes(const kvq_cache* cache, int32_t num_q_heads, int32_t budget) {
+  if (!cache || num_q_heads < 1 || cache->num_kv_heads < 1 || cache->num_seqs < 0 || budget < 1) return 0;
+  kvq::Geom g = kvq::make_geom(*cache);
+  return kvq::decode_pages_workspace(g, num_q_heads, kvq::decode_pages_splits(g, budget, num_sms()));
+}
+
+kvq_status kvq_decode_attention_pages(const kvq_cache* cache, const void* q, int32_t num_q_heads, float sm_scale,
+                                      const int32_t* page_list, const int32_t* list_len, int32_t budget, void* out,
+                                      void* ws, size_t ws_bytes, kvq_stream_t stream) {
+  g_err[0] = 0;
+  kvq_status s = check_cache(cache);
+  if (s == KVQ_OK) s = check_q_heads(cache, num_q_heads);
+  if (s != KVQ_OK) return s;
+  if (budget < 1) return fail(KVQ_ERR_INVALID_ARG, "budget %d < 1", budget);
+  if (!(sm_scale > 0.0f) || !(sm_scale < INFINITY)) return fail(KVQ_ERR_INVALID_ARG, "sm_scale must be positive and finite");
+  if (cache->num_seqs == 0) return KVQ_OK;
+  if (!q || !out || !page_list || !list_len) return fail(KVQ_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(q, 16) || !aligned(out, 16)) return fail(KVQ_ERR_INVALID_ARG, "q / out must be 16-byte aligned");
+  kvq::Geom g = kvq::make_geom(*cache);
+  kvq::PagesArgs a{};
+  a.q = (const uint16_t*)q;
+  a.Hq = num_q_heads;
+  a.Gq = num_q_heads / cache->num_kv_heads;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.list = page_list;
+  a.list_len = list_len;
+  a.budget = budget;
+  a.nsplit = kvq::decode_pages_splits(g, budget, num_sms());
+  a.out = (uint16_t*)out;
+  const size_t need = kvq::decode_pages_workspace(g, num_q_heads, a.nsplit);
+  if (ws_bytes < need || !ws) return fail(KVQ_ERR_WORKSPACE, "decode workspace %zu < %zu bytes", ws_bytes, need);
+  if (!aligned(ws, 256)) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  cudaError_t e = kvq::launch_decode_pages(g, a, ws, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_decode_attention_pages");
+  return KVQ_OK;
+}
+
 kvq_status kvq_dequantize(const kvq_cache* cache, int32_t seq, int32_t seq_len_host, int32_t start, int32_t count,
                           float* k_out, float* v_out, kvq_stream_t stream) {
   g_err[0] = 0;

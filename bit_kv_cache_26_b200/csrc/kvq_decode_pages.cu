@@ -1,0 +1,678 @@
+// Decode attention over chosen pages of the quantized paged cache: per (sequence, KV head) a list
+// of pages, softmax(q . K_hat^T) V_hat over their tokens only, in the cache's 2- or 4-bit codes.
+//
+// Per CTA one (sequence, KV head, split of the list); each warp streams its entries' sub-blocks
+// through a ring of shared-memory stages (cp.async.bulk, bounded mbarrier waits).
+//
+//   K, per page with per-channel scale s_d and zero z_d, T_j = q . M_K[j] (once per CTA):
+//     q.k_t = sum_d (q_d s_d) code_td + sum_d q_d z_d + T[idx_t]
+//   V, per token with per-group scale s_tg and zero z_tg, W_j = sum of p over tokens with pattern j:
+//     sum_t p_t v_t = sum_t (p_t s_tg) code_td + sum_t p_t z_tg + sum_j W_j M_V[j]
+//
+// The code sums are m16n8k16 products with the codes as the fp16 A operand.  A code field masked
+// out of its word is an fp16 subnormal as it stands: code * 2^S * 2^-24 for a field at bit S of a
+// half word (S <= 6, so it fits the ten mantissa bits), which the tensor cores multiply exactly.
+// One AND per pair of codes; the powers of two of the four fields of a 16x16 tile separate into a
+// row factor (undone on the sums) and a column factor (folded into B).  B is q s or p s in fp16
+// hi + lo parts (22 bits; columns = query head x {hi, lo}), from a query scaled by a power of two
+// to [16, 32): scales up to 2000 for K and 1000 for V fit fp16; past them the output is not finite
+// and KVQ_DEV_RANGE is set.
+//
+// The newest incomplete page takes its keys from the K tail, exact 16-bit operands of the same
+// products.  W is summed without atomics: lanes whose tokens share a pattern take turns in token
+// order, so results do not depend on timing.
+#include <algorithm>
+#include <atomic>
+
+#include "kvq_common.cuh"
+#include "kvq_internal.h"
+#include "kvq_pipe.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kStages = 2;   // ring stages per warp
+constexpr int kNW = 4;       // warps per CTA
+constexpr int kPexRow = 36;  // padded row of the p exchange (floats)
+constexpr float kVFac = 64.0f;  // p s is scaled by it before fp16
+
+template <int BITS>
+struct Code {
+  static constexpr float kRow = BITS == 2 ? 4.0f : 16.0f;  // factor of rows 8..15 of a tile
+  static constexpr float kCol = BITS == 2 ? 16.0f : 1.0f;  // factor of columns 8..15
+};
+
+// The A registers of tile half `odd` of word w (2-bit: two tiles per word; 4-bit: one).
+template <int BITS>
+__device__ __forceinline__ void frag16(uint32_t w, int odd, uint32_t (&a)[4]) {
+  if constexpr (BITS == 2) {
+    if (odd) w >>= 8;
+    a[0] = w & 0x00030003u;
+    a[1] = w & 0x000C000Cu;
+    a[2] = w & 0x00300030u;
+    a[3] = w & 0x00C000C0u;
+  } else {
+    const uint32_t y = w >> 8;
+    a[0] = w & 0x000F000Fu;
+    a[1] = w & 0x00F000F0u;
+    a[2] = y & 0x000F000Fu;
+    a[3] = y & 0x00F000F0u;
+  }
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// fp16 pair of the hi parts of v (its fp32 values cut to 11 significant bits) or, on lanes of a lo
+// column, of the remainders: lo_sel = (0, 0) and sign 0 for hi, (1, 1) and the sign bit for lo.
+__device__ __forceinline__ uint32_t split16(unsigned long long v, unsigned long long lo_sel, uint32_t sign) {
+  float v0, v1, r0, r1;
+  upk(v, v0, v1);
+  const float t0 = __uint_as_float((__float_as_uint(v0) & 0xFFFFE000u) ^ sign);
+  const float t1 = __uint_as_float((__float_as_uint(v1) & 0xFFFFE000u) ^ sign);
+  upk(fma2(lo_sel, v, pk(t0, t1)), r0, r1);
+  uint32_t h;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(r1), "f"(r0));
+  return h;
+}
+
+struct PagesSmem {
+  int bars, qk, qinv, T, W, pex, total;
+};
+__host__ __device__ inline PagesSmem pages_smem(int sub_bytes, int NT, int P) {
+  PagesSmem s;
+  const int NH = NT * 4;
+  // the ring; the merge at the end reuses its place
+  const int merge = (kNW * NH * kD + 2 * kNW * NH + kNW * NH * 4 + P * NH + NH * kNW) * 4;
+  int o = max(kNW * kStages * sub_bytes, merge);
+  o = (o + 15) & ~15;
+  s.bars = o; o += kNW * kStages * 8;
+  s.qk = o; o += NH * kD * 4;                // query in the quantized space, scaled, KSC order
+  s.qinv = o; o += NH * 4;                   // its inverse power of two per head
+  s.T = o; o += NH * P * 4;                  // T[head][j], scaled as the query
+  s.W = o; o += kNW * NH * (P + 1) * 4;      // per-warp pattern weights (+1: tokens stored raw)
+  o = (o + 15) & ~15;
+  s.pex = o; o += kNW * NH * kPexRow * 4;    // per-warp p exchange
+  s.total = o;
+  return s;
+}
+
+template <int BITS, int NT>
+__global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArgs a) {
+  constexpr int NH = NT * 4, WPL = BITS * 4;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gq = lane >> 2, tig = lane & 3;
+  const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int64_t grp = (int64_t)b * g.H + h;
+  const int Gq = a.Gq, P = g.P, P1 = P + 1;
+  const int sub_bytes = (int)g.sub_bytes;
+  const PagesSmem sp = pages_smem(sub_bytes, NT, P);
+  uint8_t* ring = smem + warp * kStages * sub_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + sp.bars) + warp * kStages;
+  float* qk = reinterpret_cast<float*>(smem + sp.qk);
+  float* qinv = reinterpret_cast<float*>(smem + sp.qinv);
+  float* T = reinterpret_cast<float*>(smem + sp.T);
+  float* Wall = reinterpret_cast<float*>(smem + sp.W);
+  float* Ww = Wall + warp * NH * P1;
+  float* pex = reinterpret_cast<float*>(smem + sp.pex) + warp * NH * kPexRow;
+  const unsigned long long lo_sel = (gq & 1) ? pk(1.f, 1.f) : 0ull;
+  const uint32_t lo_sign = (gq & 1) ? 0x80000000u : 0u;
+
+  int L = g.seq_len[b];
+  int n_list = a.list_len[grp];
+  const bool teller = threadIdx.x == 0 && split == 0;
+  if (L < 0 || L > (int64_t)g.maxp * kG) {
+    if (teller) set_status(g.status, KVQ_DEV_OVERFLOW);
+    L = 0;
+  }
+  if (n_list < 0 || n_list > a.budget) {
+    if (teller) set_status(g.status, KVQ_DEV_OVERFLOW);
+    n_list = 0;
+  }
+  int set = g.seq_to_set ? g.seq_to_set[b] : 0;
+  if (set < 0 || set >= g.S) {
+    if (teller) set_status(g.status, KVQ_DEV_BAD_SET);
+    set = 0;
+    n_list = 0;
+  }
+  const int nfull = L / kG, ntail = L % kG, npages = nfull + (ntail > 0);
+  const int per = (n_list + a.nsplit - 1) / a.nsplit;
+  const int e0 = min(n_list, split * per), e1 = min(n_list, e0 + per);
+  const size_t sh = (size_t)set * g.H + h;
+  const int Pe = p_eff(g, (int)sh);
+  const float* MK = g.kpat + sh * P * kD;
+  const int64_t row0 = ((int64_t)b * a.Hq + (int64_t)h * Gq) * a.nsplit + split;  // partial row of head 0; + hh * nsplit
+
+  if (e0 < e1) {
+    // entries of this warp: e0 + warp + kNW * i.  Lane l of window w holds entry 32 w + l: the physical
+    // page, -1 where the entry names none, and whether it is the newest incomplete page.
+    const int my_n = (e1 - e0 - warp + kNW - 1) / kNW;
+    const int32_t* list = a.list + grp * a.budget + e0 + warp;
+    unsigned tails = 0;
+    auto load_ids = [&](int base) -> int {
+      const int i = base + lane;
+      int phys = -1, lp = -1;
+      if (i < my_n) {
+        lp = list[kNW * i];
+        if (lp >= 0 && lp < npages) phys = g.page_table[(int64_t)b * g.maxp + lp];
+        if (phys < 0 || phys >= g.npages) {
+          set_status(g.status, KVQ_DEV_BAD_PAGE);
+          phys = -1;
+        }
+      }
+      tails = __ballot_sync(kFull, phys >= 0 && lp == nfull);
+      return phys;
+    };
+    int ids = load_ids(0);
+    auto fetch = [&](int st, int phys) {  // lane 0
+      if (phys >= 0) {
+        mbar_expect_tx(&bars[st], sub_bytes);
+        bulk_g2s(ring + st * sub_bytes, g.pool + (size_t)phys * g.page_bytes + (size_t)h * sub_bytes, sub_bytes, &bars[st]);
+      } else {
+        mbar_arrive(&bars[st]);
+      }
+    };
+    if (lane < kStages) mbar_init(&bars[lane], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+    unsigned skips = 0, tail_st = 0;  // per stage
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) {
+      const int phys = __shfl_sync(kFull, ids, i);
+      if (i < my_n) {
+        if (phys < 0) skips |= 1u << i;
+        if (tails >> i & 1) tail_st |= 1u << i;
+        if (lane == 0) fetch(i, phys);
+      }
+    }
+
+    // ---- queries, T, zeroed W (over the first copies)
+    for (int hh = warp; hh < NH; hh += kNW) {
+      float v[4], m = 0.f;
+      const uint16_t* src = a.q + ((int64_t)b * a.Hq + (int64_t)h * Gq + min(hh, Gq - 1)) * kD;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = hh < Gq ? load_elem(src + lane + 32 * k, g.dtype) : 0.f;
+      if (g.tx) {
+        fwht_warp(v, lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = v[k] * __ldg(g.kcol + sh * kD + lane + 32 * k) * 0.0078125f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m = fmaxf(m, fabsf(v[k]));
+      m = warp_max(m);
+      const int e = (int)(__float_as_uint(m) >> 23) - 127;  // exponent of the largest
+      const bool plain = m == 0.f || e > 100 || e < -100;
+      const float f = plain ? 1.f : __uint_as_float((uint32_t)(127 + 4 - e) << 23);
+      if (lane == 0) qinv[hh] = plain ? 1.f : __uint_as_float((uint32_t)(127 - 4 + e) << 23);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int ch = lane + 32 * k;
+        qk[hh * kD + ksc_pos(ch)] = v[k] * f * ((ch & 8) ? 1.0f / Code<BITS>::kCol : 1.0f);
+      }
+    }
+    for (int i = threadIdx.x; i < kNW * NH * P1; i += blockDim.x) Wall[i] = 0.f;
+    __syncthreads();
+    for (int hg = 0; hg < NT; ++hg) {
+      float qv[4][4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          qv[x][e] = qk[(4 * hg + x) * kD + ksc_pos(4 * lane + e)] * ((4 * lane & 8) ? Code<BITS>::kCol : 1.0f);
+      for (int j0 = warp; j0 < Pe; j0 += 8 * kNW) {
+        float4 m4[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int j = j0 + u * kNW;
+          m4[u] = j < Pe ? __ldg(reinterpret_cast<const float4*>(MK + (size_t)j * kD) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int j = j0 + u * kNW;
+          float t[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            t[x] = fmaf(qv[x][3], m4[u].w, fmaf(qv[x][2], m4[u].z, fmaf(qv[x][1], m4[u].y, qv[x][0] * m4[u].x)));
+            t[x] = warp_sum(t[x]);
+          }
+          if (lane < 4 && j < Pe) T[(4 * hg + lane) * P + j] = lane == 0 ? t[0] : lane == 1 ? t[1] : lane == 2 ? t[2] : t[3];
+        }
+      }
+    }
+    __syncthreads();
+
+    // ---- per-thread state (head of tile j: 4 j + tig)
+    float accv[NT][8][4], zacc[NT][4], mrun[NT], lrun[NT], scl[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      mrun[j] = -INFINITY;
+      lrun[j] = 0.f;
+      scl[j] = a.scale_log2 * qinv[4 * j + tig];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) zacc[j][u] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) accv[j][mt][u] = 0.f;
+    }
+
+    int stuck_at = -1;
+    for (int i = 0; i < my_n; ++i) {
+      const int st = i % kStages;
+      const bool ok = mbar_wait(&bars[st], (i / kStages) & 1, g.wait_limit);
+      if (!__all_sync(kFull, ok)) { stuck_at = i; break; }
+      uint8_t* pgp = ring + st * sub_bytes;
+      if (!(skips >> st & 1)) {
+        const bool tail = tail_st >> st & 1;
+        float sc[NT][4];
+        if (!tail) {
+          // ---- K: scores of the page's 32 tokens
+          uint32_t kw[WPL];
+#pragma unroll
+          for (int c = 0; c < WPL / 4; ++c) {
+            const uint4 t = reinterpret_cast<const uint4*>(pgp + c * 512)[lane];
+            kw[4 * c] = t.x; kw[4 * c + 1] = t.y; kw[4 * c + 2] = t.z; kw[4 * c + 3] = t.w;
+          }
+          const float4* ks4 = reinterpret_cast<const float4*>(pgp + g.off_ks) + tig;
+          const float4* kz4 = reinterpret_cast<const float4*>(pgp + g.off_kz) + tig;
+          const uint32_t kidx4 = *reinterpret_cast<const uint32_t*>(pgp + g.off_kidx + gq * 4);
+          float krow[4] = {1.f, 1.f, 1.f, 1.f};
+          if (g.tx) {
+            const float4 kr = *reinterpret_cast<const float4*>(pgp + g.off_krow + gq * 16);
+            krow[0] = kr.x; krow[1] = kr.y; krow[2] = kr.z; krow[3] = kr.w;
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            unsigned long long za2 = 0ull, zb2 = 0ull;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              const float4 s4 = ks4[ks * 4], z4 = kz4[ks * 4];
+              const float4 q4 = reinterpret_cast<const float4*>(qk + (4 * j + (gq >> 1)) * kD)[ks * 4 + tig];
+              const unsigned long long qa = pk(q4.x, q4.y), qb = pk(q4.z, q4.w);
+              za2 = fma2(qa, pk(z4.x, z4.y), za2);
+              zb2 = fma2(qb, pk(z4.z, z4.w), zb2);
+              const uint32_t b0 = split16(mul2(qa, pk(s4.x, s4.y)), lo_sel, lo_sign);
+              const uint32_t b1 = split16(mul2(qb, pk(s4.z, s4.w)), lo_sel, lo_sign);
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt) {
+                uint32_t f[4];
+                frag16<BITS>(BITS == 2 ? kw[mt * 4 + ks / 2] : kw[mt * 8 + ks], ks & 1, f);
+                mma_f16(acc[mt], f, b0, b1);
+              }
+            }
+            // zero term of head 4 j + gq / 2: over the 4 tig lanes, then to the lanes of head 4 j + tig
+            float z0, z1, z2, z3;
+            upk(za2, z0, z1);
+            upk(zb2, z2, z3);
+            float zk = fmaf(z2 + z3, Code<BITS>::kCol, z0 + z1);
+            zk += __shfl_xor_sync(kFull, zk, 1);
+            zk += __shfl_xor_sync(kFull, zk, 2);
+            zk = __shfl_sync(kFull, zk, 8 * tig);
+            constexpr float f0 = 16777216.0f, f8 = 16777216.0f / Code<BITS>::kRow;
+            sc[j][0] = fmaf(acc[0][0] + acc[0][1], f0, zk);
+            sc[j][1] = fmaf(acc[0][2] + acc[0][3], f8, zk);
+            sc[j][2] = fmaf(acc[1][0] + acc[1][1], f0, zk);
+            sc[j][3] = fmaf(acc[1][2] + acc[1][3], f8, zk);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int idx = min((int)((kidx4 >> (8 * u)) & 0xff), Pe - 1);
+              sc[j][u] = (sc[j][u] + T[(4 * j + tig) * P + idx]) * (krow[u] * scl[j]);
+            }
+          }
+        } else {
+          // ---- K tail: exact keys; tokens that are not there yet score -inf and store nothing of V
+          const uint16_t* kt = g.k_tail + grp * kG * kD;
+          {
+            const int t = lane;
+            if (t >= ntail) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                reinterpret_cast<float*>(pgp + g.off_vs)[vsc_pos(t, u)] = 0.f;
+                reinterpret_cast<float*>(pgp + g.off_vz)[vzc_pos(t, u)] = 0.f;
+              }
+              pgp[g.off_vidx + tok_pos(t)] = (uint8_t)kRawIndex;
+              if (g.tx) reinterpret_cast<float*>(pgp + g.off_vrow)[tok_pos(t)] = 0.f;
+            }
+            __syncwarp();
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            const int hq = 4 * j + (gq >> 1);
+            const bool has = hq < Gq && !(gq & 1);
+            const uint16_t* qr = a.q + ((int64_t)b * a.Hq + (int64_t)h * Gq + min(hq, Gq - 1)) * kD + 2 * tig;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint32_t b0 = has ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks) : 0u;
+              const uint32_t b1 = has ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8) : 0u;
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt) {
+                const uint16_t* kr = kt + (16 * mt + gq) * kD + 16 * ks + 2 * tig;
+                uint32_t f[4];
+                f[0] = *reinterpret_cast<const uint32_t*>(kr);
+                f[1] = *reinterpret_cast<const uint32_t*>(kr + 8 * kD);
+                f[2] = *reinterpret_cast<const uint32_t*>(kr + 8);
+                f[3] = *reinterpret_cast<const uint32_t*>(kr + 8 * kD + 8);
+                if (g.dtype == KVQ_BF16) mma_bf16(acc[mt], f, b0, b1);
+                else mma_f16(acc[mt], f, b0, b1);
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              sc[j][u] = gq + 8 * u < ntail ? acc[u >> 1][2 * (u & 1)] * a.scale_log2 : -INFINITY;
+          }
+        }
+        const uint32_t vidx4 = *reinterpret_cast<const uint32_t*>(pgp + g.off_vidx + gq * 4);
+        float vrow[4] = {1.f, 1.f, 1.f, 1.f};
+        if (g.tx) {
+          const float4 vr = *reinterpret_cast<const float4*>(pgp + g.off_vrow + gq * 16);
+          vrow[0] = vr.x; vrow[1] = vr.y; vrow[2] = vr.z; vrow[3] = vr.w;
+        }
+        const float4* vz4 = reinterpret_cast<const float4*>(pgp + g.off_vz) + gq;
+        const float4 vz[4] = {vz4[0], vz4[8], vz4[16], vz4[24]};
+        // turn of this lane among the lanes of the same head whose token u has the same pattern
+        int vi[4], turn[4], turns = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          vi[u] = min((int)((vidx4 >> (8 * u)) & 0xff), P);
+          const unsigned same = __match_any_sync(kFull, vi[u]) & (0x11111111u << tig);
+          turn[u] = __popc(same & ((1u << lane) - 1u));
+          turns = max(turns, turn[u]);
+        }
+        turns = __reduce_max_sync(kFull, (unsigned)turns);
+
+        // ---- online softmax (base 2), per head 4 j + tig over the 32 tokens
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int hh = 4 * j + tig;
+          const bool real = hh < Gq;
+          float pm = fmaxf(fmaxf(sc[j][0], sc[j][1]), fmaxf(sc[j][2], sc[j][3]));
+          pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 4));
+          pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 8));
+          pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 16));
+          const float mnew = fmaxf(mrun[j], pm);
+          const float msafe = mnew == -INFINITY ? 0.f : mnew;
+          const float alpha = ex2(mrun[j] - msafe);
+          if (__any_sync(kFull, alpha != 1.0f)) {
+            lrun[j] *= alpha;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) zacc[j][u] *= alpha;
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) accv[j][mt][u] *= alpha;
+            for (int jj = gq; jj < Pe; jj += 8) Ww[hh * P1 + jj] *= alpha;
+            __syncwarp();
+          }
+          mrun[j] = mnew;
+          float pv[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float p = real ? ex2(sc[j][u] - msafe) : 0.f;
+            lrun[j] += p;
+            pv[u] = p * vrow[u];
+            zacc[j][0] = fmaf(pv[u], vz[u].x, zacc[j][0]);
+            zacc[j][1] = fmaf(pv[u], vz[u].y, zacc[j][1]);
+            zacc[j][2] = fmaf(pv[u], vz[u].z, zacc[j][2]);
+            zacc[j][3] = fmaf(pv[u], vz[u].w, zacc[j][3]);
+          }
+          // tokens 8..15 of each 16 are columns with a factor of their own
+          constexpr float f0 = kVFac, f8 = kVFac / Code<BITS>::kCol;
+          *reinterpret_cast<float4*>(pex + hh * kPexRow + gq * 4) = make_float4(pv[0] * f0, pv[1] * f8, pv[2] * f0, pv[3] * f8);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            for (int r = 0; r <= turns; ++r) {
+              if (turn[u] == r) Ww[hh * P1 + vi[u]] += pv[u];
+              __syncwarp();
+            }
+        }
+        __syncwarp();
+
+        // ---- V: p-weighted codes
+        uint32_t vw[WPL];
+#pragma unroll
+        for (int c = 0; c < WPL / 4; ++c) {
+          const uint4 t = reinterpret_cast<const uint4*>(pgp + g.off_vc + c * 512)[lane];
+          vw[4 * c] = t.x; vw[4 * c + 1] = t.y; vw[4 * c + 2] = t.z; vw[4 * c + 3] = t.w;
+        }
+        const float4* vs4 = reinterpret_cast<const float4*>(pgp + g.off_vs) + tig;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const float* prow = pex + (4 * j + (gq >> 1)) * kPexRow;
+          const float4 pa = *reinterpret_cast<const float4*>(prow + (2 * tig) * 4);
+          const float4 pb = *reinterpret_cast<const float4*>(prow + (2 * tig + 1) * 4);
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            const unsigned long long p01 = ks ? pk(pa.z, pb.z) : pk(pa.x, pb.x);
+            const unsigned long long p23 = ks ? pk(pa.w, pb.w) : pk(pa.y, pb.y);
+            const float4 s0 = vs4[(ks * 4 + 0) * 4], s1 = vs4[(ks * 4 + 1) * 4], s2 = vs4[(ks * 4 + 2) * 4],
+                         s3 = vs4[(ks * 4 + 3) * 4];
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              const uint32_t b0 = split16(mul2(p01, pk((&s0.x)[q4], (&s1.x)[q4])), lo_sel, lo_sign);
+              const uint32_t b1 = split16(mul2(p23, pk((&s2.x)[q4], (&s3.x)[q4])), lo_sel, lo_sign);
+#pragma unroll
+              for (int mh = 0; mh < 2; ++mh) {
+                const int mt = q4 * 2 + mh;
+                uint32_t f[4];
+                frag16<BITS>(BITS == 2 ? vw[mt] : vw[mt * 2 + ks], ks, f);
+                mma_f16(accv[j][mt], f, b0, b1);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      // refill this stage with the entry kStages ahead
+      const int nxt = i + kStages;
+      if ((nxt & 31) == 0) ids = load_ids(nxt);
+      const int phys = __shfl_sync(kFull, ids, nxt & 31);
+      if (nxt < my_n) {
+        skips = (skips & ~(1u << st)) | (phys < 0 ? 1u << st : 0u);
+        tail_st = (tail_st & ~(1u << st)) | ((tails >> (nxt & 31) & 1) << st);
+        if (lane == 0) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          fetch(st, phys);
+        }
+      }
+      __syncwarp();
+    }
+    if (stuck_at >= 0) {
+      if (lane == 0) set_status(g.status, KVQ_DEV_TIMEOUT);
+      // the copies already issued land before the shared memory is reused or released
+      for (int i = stuck_at; i < my_n && i < stuck_at + kStages; ++i) (void)mbar_wait(&bars[i % kStages], (i / kStages) & 1);
+    }
+
+    // ---- merge the warps and write the partials
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        lrun[j] += __shfl_xor_sync(kFull, lrun[j], o);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) zacc[j][u] += __shfl_xor_sync(kFull, zacc[j][u], o);
+      }
+    }
+    __syncthreads();  // every warp is done with its ring
+    float* mo = reinterpret_cast<float*>(smem);  // [kNW][NH][128]
+    float* mm = mo + kNW * NH * kD;              // [kNW][NH] max
+    float* ml = mm + kNW * NH;                   // [kNW][NH] sum
+    float* mz = ml + kNW * NH;                   // [kNW][NH][4]
+    float* wc = mz + kNW * NH * 4;               // [P][NH] merged pattern weights
+    float* fsh = wc + P * NH;                    // [NH][kNW] warp weights
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int hh = 4 * j + tig;
+      constexpr float f0 = 16777216.0f / kVFac, f8 = 16777216.0f / kVFac / Code<BITS>::kRow;
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        mo[(warp * NH + hh) * kD + 16 * mt + gq] = (accv[j][mt][0] + accv[j][mt][1]) * f0;
+        mo[(warp * NH + hh) * kD + 16 * mt + gq + 8] = (accv[j][mt][2] + accv[j][mt][3]) * f8;
+      }
+      if (gq == 0) {
+        mm[warp * NH + hh] = mrun[j];
+        ml[warp * NH + hh] = lrun[j];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mz[(warp * NH + hh) * 4 + u] = zacc[j][u];
+      }
+    }
+    __syncthreads();
+    for (int hh = warp; hh < Gq; hh += kNW) {
+      float M = -INFINITY, Ls = 0.f, f[kNW];
+#pragma unroll
+      for (int w = 0; w < kNW; ++w) M = fmaxf(M, mm[w * NH + hh]);
+#pragma unroll
+      for (int w = 0; w < kNW; ++w) {
+        f[w] = mm[w * NH + hh] == -INFINITY ? 0.f : ex2(mm[w * NH + hh] - M);
+        Ls += f[w] * ml[w * NH + hh];
+        if (lane == w) fsh[hh * kNW + w] = f[w];
+      }
+      if (lane == 0) reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(M, Ls);
+      for (int jj = lane; jj < Pe; jj += 32) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kNW; ++w) s += f[w] * Wall[(w * NH + hh) * P1 + jj];
+        wc[jj * NH + hh] = s;
+      }
+    }
+    __syncthreads();
+    // thread = channel; each M_V value is read once per CTA
+    {
+      const int c = threadIdx.x;
+      const float* mv = g.vpat + sh * P * kD + c;
+      float o[NH];
+#pragma unroll
+      for (int i = 0; i < NH; ++i) o[i] = 0.f;
+#pragma unroll 8
+      for (int j = 0; j < Pe; ++j) {
+        const float m = __ldg(mv + (size_t)j * kD);
+#pragma unroll
+        for (int i = 0; i < NH; ++i) o[i] = fmaf(wc[j * NH + i], m, o[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+        if (i >= Gq) break;
+#pragma unroll
+        for (int w = 0; w < kNW; ++w)
+          o[i] = fmaf(fsh[i * kNW + w], mo[(w * NH + i) * kD + c] + mz[(w * NH + i) * 4 + (c >> 5)], o[i]);
+        a.part_o[(row0 + (int64_t)i * a.nsplit) * kD + c] = o[i];
+      }
+    }
+  } else {
+    // nothing of the list falls to this CTA
+    for (int hh = threadIdx.x; hh < Gq; hh += blockDim.x)
+      reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(-INFINITY, 0.f);
+  }
+
+  // ---- the CTA that completes a group merges its splits and writes the output
+  __shared__ int last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(a.arrivals + grp, 1) == a.nsplit - 1;
+    if (last) a.arrivals[grp] = 0;  // ready for the next call
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int hh = warp; hh < Gq; hh += kNW) {
+    const int64_t row = (int64_t)b * a.Hq + (int64_t)h * Gq + hh, base = row * a.nsplit;
+    uint16_t* outp = a.out + row * kD;
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + base;
+    float M = -INFINITY;
+    for (int s = lane; s < a.nsplit; s += 32) M = fmaxf(M, __ldcg(ml + s).x);
+    M = warp_max(M);
+    float Ls = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    if (M > -INFINITY) {
+      for (int s0 = 0; s0 < a.nsplit; s0 += 32) {
+        float fs = 0.f;
+        if (s0 + lane < a.nsplit) {
+          const float2 x = __ldcg(ml + s0 + lane);
+          fs = x.x == -INFINITY ? 0.f : ex2(x.x - M);
+          Ls = fmaf(fs, x.y, Ls);
+        }
+        const int n = min(32, a.nsplit - s0);
+        for (int i = 0; i < n; ++i) {
+          const float f = __shfl_sync(kFull, fs, i);
+          if (f == 0.f) continue;  // a split without entries has written no row
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[k] = fmaf(f, __ldcg(a.part_o + (base + s0 + i) * kD + lane + 32 * k), o[k]);
+        }
+      }
+      Ls = warp_sum(Ls);
+      const float inv = 1.0f / Ls;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] *= inv;
+      if (g.tx) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] *= g.vcol[sh * kD + lane + 32 * k];
+        fwht_warp(o, lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] *= 0.0078125f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!isfinite(o[k])) set_status(g.status, KVQ_DEV_RANGE);
+      outp[lane + 32 * k] = g.dtype == KVQ_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(o[k])) : __half_as_ushort(__float2half_rn(o[k]));
+    }
+  }
+}
+
+template <int BITS, int NT>
+cudaError_t launch_one(const Geom& g, const PagesArgs& a, cudaStream_t st) {
+  const int smem = pages_smem((int)g.sub_bytes, NT, g.P).total;
+  cudaError_t e = cudaFuncSetAttribute(decode_pages_kernel<BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  decode_pages_kernel<BITS, NT><<<dim3(a.nsplit, g.H, g.B), kNW * 32, smem, st>>>(g, a);
+  return cudaGetLastError();
+}
+
+template <int BITS>
+cudaError_t launch_bits(const Geom& g, const PagesArgs& a, cudaStream_t st) {
+  switch ((a.Gq + 3) / 4) {
+    case 1: return launch_one<BITS, 1>(g, a, st);
+    case 2: return launch_one<BITS, 2>(g, a, st);
+    case 3: return launch_one<BITS, 3>(g, a, st);
+    default: return launch_one<BITS, 4>(g, a, st);
+  }
+}
+
+}  // namespace
+
+// Splits of the list: four CTAs per SM, each with 8 entries or more (two per warp).
+int decode_pages_splits(const Geom& g, int budget, int num_sms) {
+  const int64_t units = std::max<int64_t>(1, (int64_t)g.B * g.H), most = std::max(1, budget / 8);
+  return (int)std::min<int64_t>(most, std::max<int64_t>(1, (4 * (int64_t)num_sms + units - 1) / units));
+}
+
+static size_t counters_bytes(const Geom& g) { return ((size_t)g.B * g.H * sizeof(int) + 255) / 256 * 256; }
+
+// Arrival counters first (their place depends on the cache alone), then the partials.
+size_t decode_pages_workspace(const Geom& g, int Hq, int nsplit) {
+  return counters_bytes(g) + (size_t)g.B * Hq * nsplit * (2 + kD) * sizeof(float);
+}
+
+cudaError_t launch_decode_pages(const Geom& g0, PagesArgs a, void* ws, cudaStream_t st) {
+  Geom g = g0;
+  g.wait_limit = page_wait_limit(g0.wait_limit);
+  a.arrivals = (int*)ws;
+  a.part_ml = (float*)((uint8_t*)ws + counters_bytes(g));
+  a.part_o = a.part_ml + 2 * (size_t)g.B * a.Hq * a.nsplit;
+  return g.bits == 2 ? launch_bits<2>(g, a, st) : launch_bits<4>(g, a, st);
+}
+
+}  // namespace kvq

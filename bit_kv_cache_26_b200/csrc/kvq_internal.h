@@ -32,6 +32,76 @@ cudaError_t launch_decode_step_mma(const Geom& g, const void* k_new, const void*
                                    float* out, cudaStream_t st);
 int decode_mma_splits(const Geom& g, int Hq, int num_sms);
 
+uint32_t page_wait_limit(uint32_t dflt);
+
+// attention over chosen pages (kvq_decode_pages.cu)
+struct PagesArgs {
+  const uint16_t* q;
+  int Hq, Gq;
+  float scale_log2;
+  const int32_t* list;      // [B][H][budget]
+  const int32_t* list_len;  // [B][H]
+  int budget, nsplit;
+  uint16_t* out;
+  float* part_ml;
+  float* part_o;
+  int* arrivals;
+};
+int decode_pages_splits(const Geom& g, int budget, int num_sms);
+size_t decode_pages_workspace(const Geom& g, int Hq, int nsplit);
+cudaError_t launch_decode_pages(const Geom& g, PagesArgs a, void* ws, cudaStream_t st);
+
+// page bounds and page selection (kvq_bounds.cu)
+cudaError_t launch_page_bounds(const Geom& g, const void* k_new, int n_new, void* bounds, cudaStream_t st);
+struct SelectArgs {
+  const uint16_t* q;
+  int Gq;
+  const uint16_t* bounds;
+  int budget, sink, recent;
+  int32_t* list;
+  int32_t* list_len;
+  int* arrivals;
+  uint32_t* keys;
+  int nsplit;
+};
+size_t select_workspace(const Geom& g);
+cudaError_t launch_select(const Geom& g, SelectArgs a, void* ws, int num_sms, cudaStream_t st);
+
+// page tables and slot maps (kvq_plan.cu)
+struct PlanArgs {
+  const int32_t* new_len;
+  const int32_t* free_pages;
+  int32_t free_cap;
+  const int32_t* free_count;
+  int32_t* free_left;
+  int32_t* cu;
+  int64_t* slot_map;
+  int32_t* positions;
+  int32_t* seq_ids;
+  int64_t max_tokens;
+  int32_t* ws;
+};
+size_t plan_workspace(const Geom& g);
+cudaError_t launch_plan(const Geom& g, const PlanArgs& a, cudaStream_t st);
+
+// norms and rotation (kvq_rope.cu)
+struct RopeRows {
+  const void* in;
+  void* out;
+  const void* weight;
+  int heads;
+  int64_t in_tok, in_head, out_tok, out_head;
+};
+struct RopeArgs {
+  RopeRows rows[3];  // queries, keys, values
+  const int32_t* pos;
+  const float* inv_freq;
+  int64_t tokens;
+  int rot, tile;
+  float eps;
+};
+cudaError_t launch_norm_rope(const RopeArgs& a, int dtype, bool interleaved, int num_sms, cudaStream_t st);
+
 // dequantize (kvq_dequant.cu)
 cudaError_t launch_dequant(const Geom& g, int seq, int start, int count, float* k_out, float* v_out,
                            cudaStream_t st);

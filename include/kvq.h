@@ -133,6 +133,7 @@ typedef enum {
 #define KVQ_DEV_BAD_SET 0x4    /* seq_to_set entry outside [0, num_sets) */
 #define KVQ_DEV_TIMEOUT 0x8    /* a bounded wait for a page copy expired; that step's output is invalid */
 #define KVQ_DEV_RANGE 0x10     /* decode: |q_d * s_d| or a V scale exceeded the fp16 operand range (~3e4) */
+#define KVQ_DEV_NO_PAGES 0x20  /* kvq_plan_pages: the free list ran out; the sequences after that got no tokens */
 
 typedef enum { KVQ_F16 = 0, KVQ_BF16 = 1 } kvq_dtype;
 typedef enum { KVQ_TX_NONE = 0, KVQ_TX_HADAMARD_VARNORM = 1 } kvq_transform;
@@ -305,6 +306,114 @@ KVQ_API size_t kvq_step_workspace_bytes(const kvq_cache* cache, int32_t num_q_he
 KVQ_API kvq_status kvq_decode_step(const kvq_cache* cache, const void* k_new, const void* v_new, const void* q,
                                    int32_t num_q_heads, float sm_scale, float* out, void* ws, size_t ws_bytes,
                                    kvq_stream_t stream);
+
+/*
+ * The rest of a serving step at long context, around the calls above:
+ *   kvq_plan_pages -> kvq_norm_rope -> kvq_page_bounds -> kvq_quantize_append (or kvq_decode_step)
+ *   -> kvq_select_pages -> kvq_decode_attention_pages.
+ */
+
+/*
+ * kvq_norm_rope -- per-head RMS norm and position rotation of queries and keys, and the values
+ * copied, from (slices of) a packed projection into the rows the cache's calls take ([PKV]
+ * Section 4.1: patterns and pages hold post-rotation keys).
+ *   A kvq_rows names one tensor of num_tokens x heads rows of 128 elements: element strides
+ *   (multiples of 8) between tokens and between heads, 16-byte aligned pointers.  heads = 0:
+ *   none.  in == out with equal strides works in place; other overlaps do not.
+ *   y_d = x_d / sqrt(mean x^2 + eps) * weight_d   (weight NULL: y = x)
+ *   with a = positions[t] * inv_freq[i], i < rot_dim / 2, and (u, v) the channels (i, i + rot_dim / 2),
+ *   or (2 i, 2 i + 1) when interleaved:  (u cos a - v sin a, v cos a + u sin a); channels >= rot_dim pass.
+ *   fp32 throughout (the angle in float64), rounded once.  Values (v->weight must be NULL) are copied.
+ *   positions [num_tokens] int32;  inv_freq [rot_dim / 2] fp32 (may be NULL when rot_dim is 0)
+ *   rot_dim: a multiple of 16, 0..128.
+ */
+typedef struct kvq_rows {
+  const void* in;
+  void* out;
+  const void* weight; /* [128] in the rows' type, or NULL */
+  int32_t heads;
+  int32_t reserved;   /* must be 0 */
+  int64_t in_tok_stride, in_head_stride, out_tok_stride, out_head_stride;
+} kvq_rows;
+KVQ_API kvq_status kvq_norm_rope(const kvq_rows* q, const kvq_rows* k, const kvq_rows* v, int32_t dtype,
+                                 int64_t num_tokens, const int32_t* positions, const float* inv_freq, int32_t rot_dim,
+                                 int32_t interleaved, float eps, kvq_stream_t stream);
+
+/*
+ * kvq_plan_pages -- page tables, slot map and positions of a batch from its request lengths.
+ * Sequence b holds seq_len[b] tokens, in pages its row of cache->page_table names, and is to get
+ * new_len[b] more.  New pages come off the top of a stack of free page ids, sequences and pages in
+ * ascending order, and are written into cache->page_table (this call writes it; seq_len advances
+ * with the append).  The new tokens of all sequences are laid out one sequence after the other:
+ *   cu_new [num_seqs + 1]   first packed token of each sequence, then the total
+ *   slot_map [max_tokens]   int64 page id * 32 + slot of each packed token
+ *   positions, seq_ids [max_tokens]  int32 position in, and index of, its sequence
+ * Entries past the total keep what they held.  free_pages [free_capacity] ids, *free_count of them
+ * free (device); *free_left = what remains (may be free_count itself: the stack is then popped).
+ * A request with a negative length or past the page table flags KVQ_DEV_OVERFLOW and gets nothing.
+ * When the tokens would pass max_tokens (KVQ_DEV_OVERFLOW) or the pages the stack
+ * (KVQ_DEV_NO_PAGES), that sequence and all after it get nothing.
+ * slot_map, positions and seq_ids are 16-byte aligned.  Workspace: kvq_plan_workspace_bytes().
+ */
+KVQ_API size_t kvq_plan_workspace_bytes(const kvq_cache* cache);
+KVQ_API kvq_status kvq_plan_pages(const kvq_cache* cache, const int32_t* new_len, const int32_t* free_pages,
+                                  int32_t free_capacity, const int32_t* free_count, int32_t* free_left,
+                                  int32_t* cu_new, int64_t* slot_map, int32_t* positions, int32_t* seq_ids,
+                                  int64_t max_tokens, void* ws, size_t ws_bytes, kvq_stream_t stream);
+
+/*
+ * kvq_page_bounds -- minimum and maximum of the keys of each page and channel, kept up as tokens
+ * arrive.  To be called with the keys of an append, before it (it places them by seq_len).
+ *   k_new   [num_seqs][n_new][num_kv_heads][128] dtype, as kvq_quantize_append takes it
+ *   bounds  [num_pages][num_kv_heads][2][128] dtype, minimum then maximum, 16-byte aligned.  A page
+ *           whose first slot is among the new ones starts afresh; the others are widened.
+ * NaN keys give NaN bounds.  A sequence that would outgrow its page table (KVQ_DEV_OVERFLOW) and a
+ * page with an invalid id (KVQ_DEV_BAD_PAGE) are left alone.
+ */
+KVQ_API kvq_status kvq_page_bounds(const kvq_cache* cache, const void* k_new, int32_t n_new, void* bounds,
+                                   kvq_stream_t stream);
+
+/*
+ * kvq_select_pages -- the pages each (sequence, KV head) attends to: all of them while there are at
+ * most `budget`, else the first `sink`, the last `recent` (the incomplete one among them) and, of
+ * those between, the budget - sink - recent with the highest score; equal scores: the lower page.
+ *   score = sum over the KV head's query heads g of max over keys k within the page's bounds of q_g . k
+ *         = sum_d W+_d max_d + W-_d min_d,  W+_d = sum_g max(q_gd, 0), W-_d = sum_g min(q_gd, 0)
+ * in fp32 and in a fixed order of operations: W halves 16 places of query heads (absent ones 0; places
+ * i and i + 8, + 4, + 2, + 1); a term is fl(fl(W+ max) + fl(W- min)); 8 neighbouring terms are halved
+ * (4, 2, 1), then the 16 sums (8, 4, 2, 1).  NaN ranks above every number; a page with an invalid id
+ * (KVQ_DEV_BAD_PAGE) below every page.
+ *   q [num_seqs][num_q_heads][128] dtype;  bounds as kvq_page_bounds keeps them
+ *   page_list [num_seqs][num_kv_heads][budget] int32: logical pages, ascending, then -1
+ *   list_len  [num_seqs][num_kv_heads] int32
+ * 1 <= recent, 0 <= sink, sink + recent <= budget.
+ * Workspace: kvq_select_workspace_bytes(), 256-byte aligned, ZERO-FILLED before its first use (its
+ * counters are left at zero again).  Two calls in flight at once on one workspace race.
+ */
+KVQ_API size_t kvq_select_workspace_bytes(const kvq_cache* cache);
+KVQ_API kvq_status kvq_select_pages(const kvq_cache* cache, const void* q, int32_t num_q_heads, const void* bounds,
+                                    int32_t budget, int32_t sink, int32_t recent, int32_t* page_list,
+                                    int32_t* list_len, void* ws, size_t ws_bytes, kvq_stream_t stream);
+
+/*
+ * kvq_decode_attention_pages -- kvq_decode_attention over listed pages only.
+ *   page_list [num_seqs][num_kv_heads][budget] int32 logical pages, in any order, list_len of them
+ *   used; a page listed twice counts twice.  The newest incomplete page takes its keys from the K
+ *   tail.  An entry that names no page of its sequence, or an invalid page id, is passed over
+ *   (KVQ_DEV_BAD_PAGE); a list_len outside 0..budget counts as 0 (KVQ_DEV_OVERFLOW).
+ *   q, out [num_seqs][num_q_heads][128] dtype: unlike kvq_decode_attention's, `out` is in the
+ *   cache's dtype (softmax and sums in fp32, rounded once).  No entries: zeros.
+ * The same inputs give the same bits on every run.  K scales above about 2000 and V scales above
+ * about 1000 leave the operands' range (KVQ_DEV_RANGE).  A page copy that does not arrive within the
+ * bounded wait flags KVQ_DEV_TIMEOUT.
+ * Workspace: kvq_decode_pages_workspace_bytes(), 256-byte aligned, ZERO-FILLED before its first use
+ * (its counters are left at zero again).  Two calls in flight at once on one workspace race.
+ */
+KVQ_API size_t kvq_decode_pages_workspace_bytes(const kvq_cache* cache, int32_t num_q_heads, int32_t budget);
+KVQ_API kvq_status kvq_decode_attention_pages(const kvq_cache* cache, const void* q, int32_t num_q_heads,
+                                              float sm_scale, const int32_t* page_list, const int32_t* list_len,
+                                              int32_t budget, void* out, void* ws, size_t ws_bytes,
+                                              kvq_stream_t stream);
 
 /*
  * kvq_dequantize -- reconstruct tokens [start, start+count) of sequence `seq`
