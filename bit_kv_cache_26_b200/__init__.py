@@ -203,41 +203,47 @@ def kvq_decode_step(cache: kvq_cache, k_new: torch.Tensor, v_new: torch.Tensor, 
 # ---------------------------------------------------------------------------
 
 _TORCH_DT = {KVQ_F16: torch.float16, KVQ_BF16: torch.bfloat16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _want(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple | None = None) -> None:
-    """A CUDA tensor of the current device, of this type and (unless None) contiguous in this shape."""
-    if t.dtype != dtype:
-        raise KvqError(KVQ_ERR_INVALID_ARG, f"{name} is {t.dtype}, not {dtype}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise KvqError(KVQ_ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current CUDA device")
-    if shape is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
-        raise KvqError(KVQ_ERR_INVALID_ARG, f"{name} must be contiguous {list(shape)}, got {list(t.shape)} with strides {list(t.stride())}")
+def _want(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int) -> int:
+    """The address of a tensor of CUDA device `dev`, of this type, contiguous in this shape; else an error."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise KvqError(KVQ_ERR_INVALID_ARG, f"{name} must be contiguous {dtype} {list(shape)} on the current CUDA device, got {t.dtype} "
+                       f"{list(t.shape)} with strides {list(t.stride())} on {t.device}")
+    return t.data_ptr()
 
 
-def _ws_bytes(ws: torch.Tensor | None) -> int:
-    return 0 if ws is None else ws.numel() * ws.element_size()
+def _here(stream) -> tuple[int, int]:
+    """The current device and the stream to use (the current one unless given)."""
+    if not torch.cuda.is_available():  # no tensor can be on a device then: the checks that follow say so
+        return 0, 0
+    dev = torch.cuda.current_device()
+    return dev, _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _rows(name: str, x: torch.Tensor | None, out: torch.Tensor | None, weight: torch.Tensor | None, dtype, tokens: int) -> kvq_rows:
-    r = kvq_rows()
+def _ws(ws: torch.Tensor | None, dev: int) -> tuple[int | None, int]:
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise KvqError(KVQ_ERR_INVALID_ARG, f"the workspace must be contiguous and on the current CUDA device, got {ws.device}")
+    return ws.data_ptr(), ws.nbytes
+
+
+def _rows(name: str, x: torch.Tensor | None, out: torch.Tensor | None, weight: torch.Tensor | None, dtype, tokens: int, dev: int) -> kvq_rows:
     if x is None:
-        return r
+        return kvq_rows()
     if out is None:
         raise KvqError(KVQ_ERR_INVALID_ARG, f"{name} has no output")
-    for label, t in ((name, x), (name + "_out", out)):
-        _want(label, t, dtype)
-        if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != x.shape[1] or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
-            raise KvqError(KVQ_ERR_INVALID_ARG, f"{label} must be [{tokens}, heads, {HEAD_DIM}] with contiguous rows, got {list(t.shape)} "
-                           f"with strides {list(t.stride())}")
-    if weight is not None:
-        _want(name + "_weight", weight, dtype, (HEAD_DIM,))
-        r.weight = weight.data_ptr()
-    r.in_, r.out, r.heads = x.data_ptr(), out.data_ptr(), x.shape[1]
-    # a dimension of one element has a stride nobody reads: whatever it says, it is none
-    r.in_tok_stride, r.in_head_stride = (x.stride(i) if x.shape[i] > 1 else 0 for i in (0, 1))
-    r.out_tok_stride, r.out_head_stride = (out.stride(i) if out.shape[i] > 1 else 0 for i in (0, 1))
-    return r
+    shape, xs, os_ = x.shape, x.stride(), out.stride()
+    if (len(shape) != 3 or shape[0] != tokens or shape[2] != HEAD_DIM or out.shape != shape or xs[2] != 1 or os_[2] != 1
+            or x.dtype is not dtype or out.dtype is not dtype or x.get_device() != dev or out.get_device() != dev):
+        raise KvqError(KVQ_ERR_INVALID_ARG, f"{name} and {name}_out must be [{tokens}, heads, {HEAD_DIM}] {dtype} with contiguous rows on the current "
+                       f"CUDA device, got {x.dtype} {list(shape)} {list(xs)} on {x.device} and {out.dtype} {list(out.shape)} {list(os_)} on {out.device}")
+    # the stride of a dimension of one element is never used, whatever it says
+    one_t, one_h = tokens == 1, shape[1] == 1
+    return kvq_rows(x.data_ptr(), out.data_ptr(), None if weight is None else _want(name + "_weight", weight, dtype, (HEAD_DIM,), dev),
+                    shape[1], 0, 0 if one_t else xs[0], 0 if one_h else xs[1], 0 if one_t else os_[0], 0 if one_h else os_[1])
 
 
 def kvq_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None, positions: torch.Tensor | None,
@@ -249,26 +255,26 @@ def kvq_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tenso
     q, k, v and their outputs are [tokens, heads, 128] of one 16-bit type; token and head strides are free (slices of a
     packed projection), rows contiguous.  Any of q, k, v may be None.  positions [tokens] int32; inv_freq [rot_dim / 2]
     fp32, whose length sets rot_dim (None: no rotation)."""
-    given = [t for t in (q, k, v) if t is not None]
-    if not given:
+    first = q if q is not None else k if k is not None else v
+    if first is None:
         return
-    dtype, tokens = given[0].dtype, given[0].shape[0]
-    if dtype not in (torch.float16, torch.bfloat16):
+    dtype, tokens = first.dtype, first.shape[0]
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise KvqError(KVQ_ERR_UNSUPPORTED, f"rows of {dtype}")
-    rq = _rows("q", q, q_out, q_weight, dtype, tokens)
-    rk = _rows("k", k, k_out, k_weight, dtype, tokens)
-    rv = _rows("v", v, v_out, None, dtype, tokens)
-    rot = 0
-    if inv_freq is not None and inv_freq.numel():
-        _want("inv_freq", inv_freq, torch.float32, (inv_freq.numel(),))
+    dev, st = _here(stream)
+    rq = _rows("q", q, q_out, q_weight, dtype, tokens, dev)
+    rk = _rows("k", k, k_out, k_weight, dtype, tokens, dev)
+    rv = _rows("v", v, v_out, None, dtype, tokens, dev)
+    rot, at, freq = 0, None, None
+    if inv_freq is not None and (q is not None or k is not None):
         rot = 2 * inv_freq.numel()
-        if q is not None or k is not None:
+        if rot:
             if positions is None:
                 raise KvqError(KVQ_ERR_INVALID_ARG, "a rotation needs positions")
-            _want("positions", positions, torch.int32, (tokens,))
-    _check(_lib.kvq_norm_rope(ctypes.byref(rq), ctypes.byref(rk), ctypes.byref(rv),
-                              KVQ_BF16 if dtype == torch.bfloat16 else KVQ_F16, tokens, _ptr(positions), _ptr(inv_freq), rot,
-                              int(interleaved), eps, _stream(stream)))
+            freq = _want("inv_freq", inv_freq, torch.float32, (rot // 2,), dev)
+            at = _want("positions", positions, torch.int32, (tokens,), dev)
+    _check(_lib.kvq_norm_rope(rq, rk, rv, KVQ_BF16 if dtype is torch.bfloat16 else KVQ_F16, tokens, at, freq, rot, bool(interleaved), eps,
+                              st))
 
 
 def kvq_plan_workspace_bytes(cache: kvq_cache) -> int:
@@ -279,26 +285,20 @@ def kvq_plan_pages(cache: kvq_cache, new_len: torch.Tensor, free_pages: torch.Te
                    free_left: torch.Tensor, cu_new: torch.Tensor, slot_map: torch.Tensor, positions: torch.Tensor,
                    seq_ids: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """Page tables, slot map and positions of a batch from its request lengths (include/kvq.h)."""
-    i32, n = torch.int32, slot_map.numel()
-    _want("new_len", new_len, i32, (cache.num_seqs,))
-    _want("free_pages", free_pages, i32, (free_pages.numel(),))
-    _want("free_count", free_count, i32, (1,))
-    _want("free_left", free_left, i32, (1,))
-    _want("cu_new", cu_new, i32, (cache.num_seqs + 1,))
-    _want("slot_map", slot_map, torch.int64, (n,))
-    _want("positions", positions, i32, (n,))
-    _want("seq_ids", seq_ids, i32, (n,))
-    _check(_lib.kvq_plan_pages(ctypes.byref(cache), _ptr(new_len), _ptr(free_pages), free_pages.numel(), _ptr(free_count),
-                               _ptr(free_left), _ptr(cu_new), _ptr(slot_map), _ptr(positions), _ptr(seq_ids), n, _ptr(ws),
-                               _ws_bytes(ws), _stream(stream)))
+    i32, n, cap, B = torch.int32, slot_map.numel(), free_pages.numel(), cache.num_seqs
+    dev, st = _here(stream)
+    _check(_lib.kvq_plan_pages(cache, _want("new_len", new_len, i32, (B,), dev), _want("free_pages", free_pages, i32, (cap,), dev), cap,
+                               _want("free_count", free_count, i32, (1,), dev), _want("free_left", free_left, i32, (1,), dev),
+                               _want("cu_new", cu_new, i32, (B + 1,), dev), _want("slot_map", slot_map, torch.int64, (n,), dev),
+                               _want("positions", positions, i32, (n,), dev), _want("seq_ids", seq_ids, i32, (n,), dev), n, *_ws(ws, dev), st))
 
 
 def kvq_page_bounds(cache: kvq_cache, k_new: torch.Tensor, n_new: int, bounds: torch.Tensor, stream=None) -> None:
     """Minimum and maximum of the keys per page and channel, with the keys of an append, before it."""
-    dt = _TORCH_DT.get(cache.dtype)
-    _want("k_new", k_new, dt, (cache.num_seqs, n_new, cache.num_kv_heads, HEAD_DIM))
-    _want("bounds", bounds, dt, (cache.num_pages, cache.num_kv_heads, 2, HEAD_DIM))
-    _check(_lib.kvq_page_bounds(ctypes.byref(cache), _ptr(k_new), n_new, _ptr(bounds), _stream(stream)))
+    dt, H = _TORCH_DT.get(cache.dtype), cache.num_kv_heads
+    dev, st = _here(stream)
+    _check(_lib.kvq_page_bounds(cache, _want("k_new", k_new, dt, (cache.num_seqs, n_new, H, HEAD_DIM), dev), n_new,
+                                _want("bounds", bounds, dt, (cache.num_pages, H, 2, HEAD_DIM), dev), st))
 
 
 def kvq_select_workspace_bytes(cache: kvq_cache) -> int:
@@ -308,13 +308,12 @@ def kvq_select_workspace_bytes(cache: kvq_cache) -> int:
 def kvq_select_pages(cache: kvq_cache, q: torch.Tensor, num_q_heads: int, bounds: torch.Tensor, budget: int, sink: int,
                      recent: int, page_list: torch.Tensor, list_len: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """The pages each (sequence, KV head) attends to, by an upper bound of its scores (workspace zero-filled before first use)."""
-    dt, B, H = _TORCH_DT.get(cache.dtype), cache.num_seqs, cache.num_kv_heads
-    _want("q", q, dt, (B, num_q_heads, HEAD_DIM))
-    _want("bounds", bounds, dt, (cache.num_pages, H, 2, HEAD_DIM))
-    _want("page_list", page_list, torch.int32, (B, H, budget))
-    _want("list_len", list_len, torch.int32, (B, H))
-    _check(_lib.kvq_select_pages(ctypes.byref(cache), _ptr(q), num_q_heads, _ptr(bounds), budget, sink, recent, _ptr(page_list),
-                                 _ptr(list_len), _ptr(ws), _ws_bytes(ws), _stream(stream)))
+    dt, B, H, i32 = _TORCH_DT.get(cache.dtype), cache.num_seqs, cache.num_kv_heads, torch.int32
+    dev, st = _here(stream)
+    _check(_lib.kvq_select_pages(cache, _want("q", q, dt, (B, num_q_heads, HEAD_DIM), dev), num_q_heads,
+                                 _want("bounds", bounds, dt, (cache.num_pages, H, 2, HEAD_DIM), dev), budget, sink, recent,
+                                 _want("page_list", page_list, i32, (B, H, budget), dev), _want("list_len", list_len, i32, (B, H), dev),
+                                 *_ws(ws, dev), st))
 
 
 def kvq_decode_pages_workspace_bytes(cache: kvq_cache, num_q_heads: int, budget: int) -> int:
@@ -324,14 +323,12 @@ def kvq_decode_pages_workspace_bytes(cache: kvq_cache, num_q_heads: int, budget:
 def kvq_decode_attention_pages(cache: kvq_cache, q: torch.Tensor, num_q_heads: int, sm_scale: float, page_list: torch.Tensor,
                                list_len: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """kvq_decode_attention over listed pages only; `out` is in the cache's dtype (workspace zero-filled before first use)."""
-    dt, B, H = _TORCH_DT.get(cache.dtype), cache.num_seqs, cache.num_kv_heads
-    budget = page_list.shape[-1]
-    _want("q", q, dt, (B, num_q_heads, HEAD_DIM))
-    _want("out", out, dt, (B, num_q_heads, HEAD_DIM))
-    _want("page_list", page_list, torch.int32, (B, H, budget))
-    _want("list_len", list_len, torch.int32, (B, H))
-    _check(_lib.kvq_decode_attention_pages(ctypes.byref(cache), _ptr(q), num_q_heads, sm_scale, _ptr(page_list), _ptr(list_len),
-                                           budget, _ptr(out), _ptr(ws), _ws_bytes(ws), _stream(stream)))
+    dt, B, H, i32, budget = _TORCH_DT.get(cache.dtype), cache.num_seqs, cache.num_kv_heads, torch.int32, page_list.shape[-1]
+    dev, st = _here(stream)
+    _check(_lib.kvq_decode_attention_pages(cache, _want("q", q, dt, (B, num_q_heads, HEAD_DIM), dev), num_q_heads, sm_scale,
+                                           _want("page_list", page_list, i32, (B, H, budget), dev),
+                                           _want("list_len", list_len, i32, (B, H), dev), budget,
+                                           _want("out", out, dt, (B, num_q_heads, HEAD_DIM), dev), *_ws(ws, dev), st))
 
 
 def kvq_dequantize(cache: kvq_cache, seq: int, seq_len_host: int, start: int, count: int,

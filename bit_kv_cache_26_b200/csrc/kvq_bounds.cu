@@ -18,6 +18,7 @@
 
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
+#include "kvq_pipe.cuh"
 
 namespace kvq {
 
@@ -98,10 +99,10 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) page_bounds_kernel(Geom g, 
 
 // ---- selection -------------------------------------------------------------------------------
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelKeys = 16;        // keys a thread keeps in registers: up to 8192 pages
-constexpr int kSelAhead = 4;        // pages in flight per 16 lanes
+constexpr int kSelAhead = 4;           // pages in flight per 16 lanes
+constexpr int kSelKeys = 8192;         // keys that fit in shared memory
 
 // fp32 -> unsigned with the same order; -0 is +0, NaN above all.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -110,75 +111,48 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-__device__ __forceinline__ unsigned long long mulp(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ unsigned long long addp(unsigned long long a, unsigned long long b) {
   unsigned long long r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ unsigned long long packf(float a, float b) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
 template <bool BF16>
 __device__ __forceinline__ unsigned long long widen(uint32_t u) {
-  if constexpr (BF16) return packf(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  if constexpr (BF16) return pk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-  return packf(f.x, f.y);
+  return pk(f.x, f.y);
 }
 
-// Block-wide sum of one value per thread; `buf` alternates between two halves so that one barrier
-// per sum is enough.
-__device__ __forceinline__ unsigned block_sum(unsigned v, unsigned (*buf)[kSelWarps], int& turn) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  v = __reduce_add_sync(kFull, v);
-  if (lane == 0) buf[turn][warp] = v;
-  __syncthreads();
-  unsigned s = lane < kSelWarps ? buf[turn][lane] : 0u;
-  turn ^= 1;
-  return __reduce_add_sync(kFull, s);
-}
-
-// Exclusive block-wide prefix of one value per thread (two barriers).
-__device__ __forceinline__ unsigned long long block_prefix(unsigned long long v, unsigned long long* buf) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long inc = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long t = __shfl_up_sync(kFull, inc, o);
-    if (lane >= o) inc += t;
-  }
-  __syncthreads();
-  if (lane == 31) buf[warp] = inc;
-  __syncthreads();
-  unsigned long long before = 0;
-  for (int w = 0; w < warp; ++w) before += buf[w];
-  return before + inc - v;
-}
-
-// Scores of pages [p0, p1) of (b, h) as ordered keys: 16 lanes per page, 8 channels per lane.
+// Scores of pages [p0, p1) of (b, h) as ordered keys, keys[p - lo_page]: 16 lanes per page, 8 channels per lane, four
+// pages in flight; their four sums over the lanes share the exchanges (after a step that halves the lanes a value
+// is spread over, each half of the lanes goes on with half of the values).
 template <bool BF16>
 __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int Gq, const uint16_t* __restrict__ bounds, int b,
-                            int h, int p0, int p1, uint32_t* keys, float* W) {
-  const int lane = threadIdx.x & 31, c = lane & 15;
-  if (threadIdx.x < 2 * kD) {  // W+ and W-
+                            int h, int p0, int p1, int lo_page, uint32_t* keys, float* W) {
+  static_assert(kSelAhead == 4, "the exchange below is written for four pages");
+  const int lane = threadIdx.x & 31, c = lane & 15, sub = lane >> 4;
+  const int32_t* table = g.page_table + (int64_t)b * g.maxp;
+  const int first = p0 + 2 * kSelAhead * (threadIdx.x >> 5) + kSelAhead * sub;
+  int phys[kSelAhead];
+  auto load_ids = [&](int p) {
+#pragma unroll
+    for (int i = 0; i < kSelAhead; ++i) {
+      phys[i] = p + i < p1 ? table[p + i] : -1;
+      if (p + i < p1 && (unsigned)phys[i] >= (unsigned)g.npages) {
+        set_status(g.status, KVQ_DEV_BAD_PAGE);
+        phys[i] = -1;
+      }
+    }
+  };
+  load_ids(first);
+  {  // W+ (threads 0..127) and W- (128..255)
     const int d = threadIdx.x & (kD - 1);
     const bool neg = threadIdx.x >= kD;
     float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float x = 0.f;
-      if (i < Gq) {
-        x = load_elem(q + ((int64_t)b * g.H * Gq + (int64_t)h * Gq + i) * kD + d, g.dtype);
-        x = x != x ? x : neg ? fminf(x, 0.f) : fmaxf(x, 0.f);
-      }
-      v[i] = x;
-    }
+    for (int i = 0; i < 16; ++i) v[i] = i < Gq ? load_elem(q + ((int64_t)b * g.H * Gq + (int64_t)h * Gq + i) * kD + d, g.dtype) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = v[i] != v[i] ? v[i] : neg ? fminf(v[i], 0.f) : fmaxf(v[i], 0.f);
 #pragma unroll
     for (int o = 8; o; o >>= 1)
 #pragma unroll
@@ -189,108 +163,177 @@ __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int G
   unsigned long long up[4], dn[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    up[e] = packf(W[8 * c + 2 * e], W[8 * c + 2 * e + 1]);
-    dn[e] = packf(W[kD + 8 * c + 2 * e], W[kD + 8 * c + 2 * e + 1]);
+    up[e] = pk(W[8 * c + 2 * e], W[8 * c + 2 * e + 1]);
+    dn[e] = pk(W[kD + 8 * c + 2 * e], W[kD + 8 * c + 2 * e + 1]);
   }
-  const int32_t* table = g.page_table + (int64_t)b * g.maxp;
-  const int hw = threadIdx.x >> 4;
-  for (int q0 = p0 + (hw & ~1); q0 < p1; q0 += 2 * kSelWarps * kSelAhead) {
+  const uint16_t* mine = bounds + (int64_t)h * 2 * kD + 8 * c;
+  const int64_t page_stride = (int64_t)g.H * 2 * kD;
+  for (int p = first; p - kSelAhead * sub < p1; p += 2 * kSelAhead * kSelWarps) {
     uint4 lo[kSelAhead], hi[kSelAhead];
-    int phys[kSelAhead];
-#pragma unroll
-    for (int i = 0; i < kSelAhead; ++i) {
-      const int p = q0 + (hw & 1) + i * 2 * kSelWarps;
-      phys[i] = p < p1 ? table[p] : -1;
-      if (p < p1 && (phys[i] < 0 || phys[i] >= g.npages)) {
-        set_status(g.status, KVQ_DEV_BAD_PAGE);
-        phys[i] = -1;
-      }
-    }
+    bool none[kSelAhead];
 #pragma unroll
     for (int i = 0; i < kSelAhead; ++i) {
       lo[i] = hi[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (phys[i] >= 0) {
-        const uint16_t* src = bounds + ((int64_t)phys[i] * g.H + h) * 2 * kD + 8 * c;
+      none[i] = phys[i] < 0;
+      if (!none[i]) {
+        const uint16_t* src = mine + phys[i] * page_stride;
         lo[i] = __ldg(reinterpret_cast<const uint4*>(src));
         hi[i] = __ldg(reinterpret_cast<const uint4*>(src + kD));
       }
     }
+    load_ids(p + 2 * kSelAhead * kSelWarps);
+    float x[kSelAhead];
 #pragma unroll
     for (int i = 0; i < kSelAhead; ++i) {
       const uint32_t* l = &lo[i].x;
       const uint32_t* u = &hi[i].x;
       unsigned long long t[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] = addp(mulp(up[e], widen<BF16>(u[e])), mulp(dn[e], widen<BF16>(l[e])));
-      const unsigned long long s = addp(addp(t[0], t[2]), addp(t[1], t[3]));
-      float a, bb;
-      asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(bb) : "l"(s));
-      float x = __fadd_rn(a, bb);
-#pragma unroll
-      for (int o = 8; o; o >>= 1) x = __fadd_rn(x, __shfl_xor_sync(kFull, x, o));
-      const int p = q0 + (hw & 1) + i * 2 * kSelWarps;
-      if (c == 0 && p < p1) keys[p] = phys[i] >= 0 ? order_key(x) : 0u;
+      for (int e = 0; e < 4; ++e) t[e] = addp(mul2(up[e], widen<BF16>(u[e])), mul2(dn[e], widen<BF16>(l[e])));
+      float s0, s1;
+      upk(addp(addp(t[0], t[2]), addp(t[1], t[3])), s0, s1);
+      x[i] = __fadd_rn(s0, s1);
+    }
+    // lanes with bit 3: pages 2 and 3; of those, lanes with bit 2: the odd one
+    const bool b3 = c & 8, b2 = c & 4;
+    const float y0 = __fadd_rn(b3 ? x[2] : x[0], __shfl_xor_sync(kFull, b3 ? x[0] : x[2], 8));
+    const float y1 = __fadd_rn(b3 ? x[3] : x[1], __shfl_xor_sync(kFull, b3 ? x[1] : x[3], 8));
+    float z = __fadd_rn(b2 ? y1 : y0, __shfl_xor_sync(kFull, b2 ? y0 : y1, 4));
+    z = __fadd_rn(z, __shfl_xor_sync(kFull, z, 2));
+    z = __fadd_rn(z, __shfl_xor_sync(kFull, z, 1));
+    const int i = (b3 ? 2 : 0) + (b2 ? 1 : 0);
+    if ((c & 3) == 0 && p + i < p1) {
+      const bool gone = b3 ? (b2 ? none[3] : none[2]) : (b2 ? none[1] : none[0]);
+      keys[p + i - lo_page] = gone ? 0u : order_key(z);
     }
   }
 }
 
-// The k largest of keys[p0 .. p1) (ties: the lower index), in index order, to list[0 .. k).
-// Thread t looks after a run of consecutive keys; up to kSelKeys of them sit in registers.  The
-// k-th largest key is found bit by bit: 32 counts over the block.
-__device__ void take_largest(const uint32_t* keys, int p0, int p1, int k, int32_t* list, unsigned (*buf)[kSelWarps],
-                             unsigned long long* buf2) {
-  const int n = p1 - p0, per = (n + kSelThreads - 1) / kSelThreads;
-  const int a0 = p0 + min(n, (int)threadIdx.x * per), a1 = min(p1, a0 + per);
-  const bool regs = per <= kSelKeys;
-  uint32_t key[kSelKeys];
-  if (regs) {
-#pragma unroll
-    for (int i = 0; i < kSelKeys; ++i) key[i] = a0 + i < a1 ? __ldcg(keys + a0 + i) : 0u;
+// Shared memory of the choice.
+struct Chooser {
+  unsigned bins[256];
+  uint4 sums[2][kSelWarps / 4];  // one value per warp, two sets
+  unsigned digit, above, count;
+};
+
+// One value per warp (the same in all its lanes) to every thread, joined by `join`; one barrier.
+template <typename F>
+__device__ __forceinline__ unsigned block_join(unsigned v, uint4* buf, F join) {
+  static_assert(kSelWarps == 8, "two 16-byte reads");
+  if ((threadIdx.x & 31) == 0) reinterpret_cast<unsigned*>(buf)[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const uint4 x = buf[0], y = buf[1];
+  return join(join(join(x.x, x.y), join(x.z, x.w)), join(join(y.x, y.y), join(y.z, y.w)));
+}
+// The sum of the warps before this one.
+__device__ __forceinline__ unsigned block_before(unsigned v, uint4* buf) {
+  if ((threadIdx.x & 31) == 0) reinterpret_cast<unsigned*>(buf)[threadIdx.x >> 5] = v;
+  __syncthreads();
+  unsigned s = 0;
+  for (int w = 0; w < (int)(threadIdx.x >> 5); ++w) s += reinterpret_cast<const unsigned*>(buf)[w];
+  return s;
+}
+
+// The k largest of keys[0 .. m) (ties: the lower index), in index order, as `base` + index to list[0 .. k); run by the
+// whole block.  The k-th largest key is found by histograms of 8 bits at a time, below the bits all keys share and until
+// the keys of a bin are exactly the ones still wanted: two or three rounds where a bit-by-bit search took eleven, each
+// as long as a round here.  The loops stay rolled: they run once per group, and fetching the instructions of unrolled
+// ones took longer than the keys.
+template <bool L2>
+__device__ void take_largest(const uint32_t* keys, int m, int k, int base, int32_t* list, Chooser& s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto load = [&](int i) -> uint32_t { return L2 ? __ldcg(keys + i) : keys[i]; };
+  uint32_t top = 0u, low = ~0u;
+#pragma unroll 4
+  for (int i = tid; i < m; i += kSelThreads) {
+    const uint32_t x = load(i);
+    top = max(top, x);
+    low = min(low, x);
   }
-  uint32_t T = 0;
-  int turn = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t cand = T | (1u << bit);
-    unsigned cnt = 0;
-    if (regs) {
-#pragma unroll
-      for (int i = 0; i < kSelKeys; ++i) cnt += key[i] >= cand;
-    } else {
-      for (int i = a0; i < a1; ++i) cnt += __ldcg(keys + i) >= cand;
+  s.bins[tid] = 0u;
+  top = block_join(__reduce_max_sync(kFull, top), s.sums[0], [](unsigned x, unsigned y) { return max(x, y); });
+  low = block_join(__reduce_min_sync(kFull, low), s.sums[1], [](unsigned x, unsigned y) { return min(x, y); });
+  int shift = 32 - __clz(top ^ low);  // bits below the ones all keys share
+  uint32_t T = shift == 32 ? 0u : top >> shift << shift;
+  unsigned want = k;                  // of the keys that agree with T above `shift`
+  bool exact = false;                 // they are all wanted
+  while (shift > 0) {
+    const int width = min(8, shift), high = shift;
+    shift -= width;
+    const uint32_t prefix = high == 32 ? 0u : T >> high, mask = (1u << width) - 1u;
+#pragma unroll 4
+    for (int i = tid; i < m; i += kSelThreads) {
+      const uint32_t x = load(i);
+      if ((high == 32 ? 0u : x >> high) == prefix) atomicAdd(&s.bins[x >> shift & mask], 1u);
     }
-    if (block_sum(cnt, buf, turn) >= (unsigned)k) T = cand;
+    __syncthreads();
+    const unsigned mine = s.bins[255 - tid];  // bins from the highest on
+    unsigned upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(kFull, upto, o);
+      if (lane >= o) upto += v;
+    }
+    upto += block_before(__shfl_sync(kFull, upto, 31), s.sums[0]);
+    if (upto >= want && upto - mine < want) {
+      s.digit = 255 - tid;
+      s.above = upto - mine;
+      s.count = mine;
+    }
+    s.bins[255 - tid] = 0u;  // (each thread's own) for the next round
+    __syncthreads();
+    T |= s.digit << shift;
+    want -= s.above;
+    exact = s.count == want;
+    if (exact) break;
+    __syncthreads();  // before s.digit is written again
   }
-  // how many above the k-th, how many equal to it (T = 0 when fewer than k keys exceed 0: all equal it)
+  // keys > T (>= T when all of those are wanted) are taken, and the first `want` that equal T
+  const uint32_t over = exact ? T - 1u : T;  // (exact leaves T > 0: there are more than k keys)
+  const int rows = (m + kSelThreads - 1) / kSelThreads;  // a warp's run: rows x 32 consecutive keys
+  const int a0 = warp * rows * 32 + lane;
   unsigned gt = 0, eq = 0;
-  for (int i = a0; i < a1; ++i) {
-    const uint32_t x = __ldcg(keys + i);
-    gt += x > T;
-    eq += x == T;
+#pragma unroll 4
+  for (int i = 0; i < rows; ++i) {
+    const int at = a0 + 32 * i;
+    const uint32_t x = at < m ? load(at) : 0u;
+    gt += at < m && x > over;
+    eq += at < m && x == T;
   }
-  const unsigned above = block_sum(gt, buf, turn);
-  const unsigned ties = k - above;
-  const unsigned long long before = block_prefix((unsigned long long)gt << 32 | eq, buf2);
-  const unsigned eq0 = (unsigned)before;
-  unsigned out = (unsigned)(before >> 32) + min(eq0, ties), e = eq0;
-  for (int i = a0; i < a1; ++i) {
-    const uint32_t x = __ldcg(keys + i);
-    const bool tie = x == T;
-    if (x > T || (tie && e < ties)) list[out++] = i;
-    e += tie;
+  unsigned out, tie;
+  if (m < 65536) {  // both counts in one exchange
+    const unsigned before = block_before(__reduce_add_sync(kFull, gt << 16 | eq), s.sums[0]);
+    out = before >> 16;
+    tie = before & 0xffffu;
+  } else {
+    out = block_before(__reduce_add_sync(kFull, gt), s.sums[0]);
+    tie = block_before(__reduce_add_sync(kFull, eq), s.sums[1]);
+  }
+  if (!exact) out += min(tie, want);
+  const unsigned below = (1u << lane) - 1u;
+  for (int i = 0; i < rows; ++i) {
+    const int at = a0 + 32 * i;
+    const uint32_t x = at < m ? load(at) : 0u;
+    const unsigned same = __ballot_sync(kFull, !exact && at < m && x == T);
+    const bool take = at < m && (x > over || ((same >> lane & 1u) && tie + __popc(same & below) < want));
+    const unsigned taken = __ballot_sync(kFull, take);
+    if (take) list[out + __popc(taken & below)] = base + at;
+    out += __popc(taken);
+    tie += __popc(same);
   }
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kSelThreads) select_pages_kernel(Geom g, SelectArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 4) select_pages_kernel(Geom g, SelectArgs a) {
   __shared__ float W[2 * kD];
-  __shared__ unsigned buf[2][kSelWarps];
-  __shared__ unsigned long long buf2[kSelWarps];
+  __shared__ Chooser chooser;
+  __shared__ __align__(16) uint32_t own_keys[kSelKeys];
   __shared__ int last;
   const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int64_t grp = (int64_t)b * g.H + h;
   int32_t* list = a.list + grp * a.budget;
   const int L = g.seq_len[b];
-  int n = (L + kG - 1) / kG;
+  int n = (int)(((int64_t)L + kG - 1) / kG);
   if (L < 0 || L > (int64_t)g.maxp * kG) {
     if (threadIdx.x == 0) set_status(g.status, KVQ_DEV_OVERFLOW);
     n = 0;
@@ -302,11 +345,14 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(Geom g, Selec
     }
     return;
   }
-  const int lo = a.sink, hi = n - a.recent, m = hi - lo;
-  const int per = (m + a.nsplit - 1) / a.nsplit;
-  const int p0 = min(hi, lo + split * per), p1 = min(hi, p0 + per);
-  uint32_t* keys = a.keys + grp * g.maxp;
-  if (p0 < p1) score_pages<BF16>(g, a.q, a.Gq, a.bounds, b, h, p0, p1, keys, W);
+  const int lo = a.sink, hi = n - a.recent, m = hi - lo, k = a.budget - a.sink - a.recent;
+  const bool local = a.nsplit == 1 && m <= kSelKeys;  // the keys never leave shared memory
+  uint32_t* keys = local ? own_keys : a.keys + grp * g.maxp;
+  if (k > 0) {
+    const int per = (m + a.nsplit - 1) / a.nsplit;
+    const int p0 = min(hi, lo + split * per), p1 = min(hi, p0 + per);
+    if (p0 < p1) score_pages<BF16>(g, a.q, a.Gq, a.bounds, b, h, p0, p1, lo, keys, W);
+  }
   if (a.nsplit > 1) {
     __threadfence();
     __syncthreads();
@@ -317,13 +363,17 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(Geom g, Selec
     __syncthreads();
     if (!last) return;
     __threadfence();
-  } else {
-    __syncthreads();
+    if (m <= kSelKeys && k > 0) {
+      for (int i = threadIdx.x; i < m; i += kSelThreads) own_keys[i] = __ldcg(keys + i);
+    }
+  }
+  __syncthreads();
+  if (k > 0) {
+    if (m <= kSelKeys) take_largest<false>(own_keys, m, k, lo, list + a.sink, chooser);
+    else take_largest<true>(keys, m, k, lo, list + a.sink, chooser);
   }
   for (int i = threadIdx.x; i < a.sink; i += kSelThreads) list[i] = i;
   for (int i = threadIdx.x; i < a.recent; i += kSelThreads) list[a.budget - a.recent + i] = hi + i;
-  const int k = a.budget - a.sink - a.recent;
-  if (k > 0) take_largest(keys, lo, hi, k, list + a.sink, buf, buf2);
   if (threadIdx.x == 0) a.list_len[grp] = a.budget;
 }
 
@@ -350,9 +400,9 @@ cudaError_t launch_select(const Geom& g, SelectArgs a, void* ws, int num_sms, cu
   const size_t groups = (size_t)g.B * g.H;
   a.arrivals = (int*)ws;
   a.keys = (uint32_t*)((uint8_t*)ws + (groups * sizeof(int) + 255) / 256 * 256);
-  // two CTAs per SM, each with 64 pages or more
+  // four CTAs per SM, each with 64 pages (one round of its warps) or more
   const int64_t most = std::max(1, g.maxp / 64);
-  a.nsplit = (int)std::min<int64_t>(most, std::max<int64_t>(1, 2 * (int64_t)num_sms / (int64_t)groups));
+  a.nsplit = (int)std::min<int64_t>(most, std::max<int64_t>(1, 4 * (int64_t)num_sms / (int64_t)groups));
   const dim3 grid(a.nsplit, g.H, g.B);
   if (g.dtype == KVQ_BF16) select_pages_kernel<true><<<grid, kSelThreads, 0, st>>>(g, a);
   else select_pages_kernel<false><<<grid, kSelThreads, 0, st>>>(g, a);

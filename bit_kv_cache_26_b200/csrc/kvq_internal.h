@@ -97,7 +97,7 @@ struct RopeArgs {
   const int32_t* pos;
   const float* inv_freq;
   int64_t tokens;
-  int rot, tile;
+  int rot, parts;  // parts: warps a token's heads are dealt to
   float eps;
 };
 cudaError_t launch_norm_rope(const RopeArgs& a, int dtype, bool interleaved, int num_sms, cudaStream_t st);

@@ -10,25 +10,28 @@
 // Everything between the load and the store is fp32 with one rounding at the end.  The angle
 // is formed in float64 as turns (pos * inv_freq / 2 pi, minus its integer part), so far
 // positions keep their phase; the sine and cosine of the remainder are fp32.
+#include <algorithm>
+
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
+#include "kvq_pipe.cuh"
 
 namespace kvq {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = kRopeThreads / 16;  // a row of 128 channels is held by 16 lanes
-constexpr int kRopeBatch = 4;                 // rows in flight per 16 lanes
-constexpr int kRopeTile = 8;                  // most tokens of a CTA: they share one table of angles
+constexpr int kRopeWarps = 4;
 
 template <bool BF16>
-__device__ __forceinline__ float2 to_f2(uint32_t u) {
-  if constexpr (BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+__device__ __forceinline__ unsigned long long widen2(uint32_t u) {
+  if constexpr (BF16) return pk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+  return pk(f.x, f.y);
 }
 template <bool BF16>
-__device__ __forceinline__ uint32_t from_f2(float a, float b) {
+__device__ __forceinline__ uint32_t narrow2(unsigned long long v) {
+  float a, b;
+  upk(v, a, b);
   if constexpr (BF16) {
     const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&r);
@@ -37,115 +40,113 @@ __device__ __forceinline__ uint32_t from_f2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// A row's 32 granules of 4 channels over 16 lanes, two each, so that a lane holds both channels of
-// each of its pairs: lane c of the rotated part takes granules c and c + rot/8 (halves) or 2c and
-// 2c + 1 (adjacent pairs); the lanes after it share the granules that pass.
+// A warp takes one token and a run of its groups of four heads (queries, keys and values apart), a row over 8 lanes:
+// two pieces of 8 channels per lane, so that a lane holds both channels of each of its pairs.  Lane c of the rotated
+// part has pieces c and c + rot/16 (halves) or 2c and 2c + 1 (adjacent pairs); the lanes after it share the pieces
+// that pass.  The token's sines and cosines are made once per warp, two per lane, and kept in registers over the heads.
 template <bool BF16, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(RopeArgs a) {
-  __shared__ __align__(16) float2 cs[kRopeTile][kD / 2];
-  const int lane16 = threadIdx.x & 15, hw = threadIdx.x >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * a.tile;
-  const int tn = (int)min((int64_t)a.tile, a.tokens - t0);
-  const int HT = a.rows[0].heads + a.rows[1].heads + a.rows[2].heads;
-  const int nrows = tn * HT;
-  const int pairs = a.rot / 2, rl = a.rot / 8;  // lanes of the rotated part
-  const bool turns = lane16 < rl;
-  const int gA = INTER ? 2 * lane16 : turns ? lane16 : 2 * rl + 2 * (lane16 - rl);
-  const int gB = INTER ? gA + 1 : turns ? lane16 + rl : gA + 1;
-  uint2 wq[2], wk[2];
-  if (a.rows[0].weight) {
-    wq[0] = *reinterpret_cast<const uint2*>((const uint16_t*)a.rows[0].weight + 4 * gA);
-    wq[1] = *reinterpret_cast<const uint2*>((const uint16_t*)a.rows[0].weight + 4 * gB);
-  }
-  if (a.rows[1].weight) {
-    wk[0] = *reinterpret_cast<const uint2*>((const uint16_t*)a.rows[1].weight + 4 * gA);
-    wk[1] = *reinterpret_cast<const uint2*>((const uint16_t*)a.rows[1].weight + 4 * gB);
-  }
-  const int dt = kRopeRows / HT, dh = kRopeRows % HT;  // one step of kRopeRows rows
-  int tok = hw / HT, head = hw % HT;
-  uint2 x[kRopeBatch][2];
-  uint16_t* dst[kRopeBatch];
-  int kind[kRopeBatch], at[kRopeBatch];  // 0 query, 1 key, 2 value, 3 none; token of the tile
-  auto load = [&](int r0) {
-#pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
-      const int r = r0 + (hw & 1) + i * kRopeRows;
-      int h = head, set = 0;
-      if (h >= a.rows[0].heads) { h -= a.rows[0].heads; set = 1; }
-      if (set == 1 && h >= a.rows[1].heads) { h -= a.rows[1].heads; set = 2; }
-      kind[i] = r < nrows ? set : 3;
-      at[i] = tok;
-      dst[i] = nullptr;
-      x[i][0] = x[i][1] = make_uint2(0u, 0u);
-      if (r < nrows) {
-        const RopeRows& R = a.rows[set];
-        const uint16_t* src = (const uint16_t*)R.in + (t0 + tok) * R.in_tok + h * R.in_head;
-        dst[i] = (uint16_t*)R.out + (t0 + tok) * R.out_tok + h * R.out_head;
-        x[i][0] = *reinterpret_cast<const uint2*>(src + 4 * gA);
-        x[i][1] = *reinterpret_cast<const uint2*>(src + 4 * gB);
-      }
-      tok += dt;
-      head += dh;
-      if (head >= HT) { head -= HT; ++tok; }
-    }
+__global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(RopeArgs a) {
+  __shared__ __align__(16) float table[kRopeWarps][2][kD / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 7, row = lane >> 3;
+  const int64_t item = (int64_t)blockIdx.x * kRopeWarps + warp;
+  const int64_t t = item / a.parts;
+  if (t >= a.tokens) return;
+  const int nq = (a.rows[0].heads + 3) / 4, nk = (a.rows[1].heads + 3) / 4, nv = (a.rows[2].heads + 3) / 4;
+  const int part = (int)(item % a.parts), per = (nq + nk + nv + a.parts - 1) / a.parts;
+  const int g0 = part * per, g1 = min(nq + nk + nv, g0 + per);
+  const int rl = a.rot / 16;  // lanes of the rotated part
+  const bool turns = c < rl;
+  const int pA = INTER ? 2 * c : turns ? c : 2 * rl + 2 * (c - rl);
+  const int pB = INTER ? pA + 1 : turns ? c + rl : pA + 1;
+
+  // the rows of group grp: this lane's two pieces, and where they go (null: no such head)
+  auto load = [&](int grp, uint4& xA, uint4& xB) -> uint16_t* {
+    const int set = grp < nq ? 0 : grp < nq + nk ? 1 : 2;
+    const RopeRows& R = a.rows[set];
+    const int h = 4 * (grp - (set == 0 ? 0 : set == 1 ? nq : nq + nk)) + row;
+    xA = xB = make_uint4(0u, 0u, 0u, 0u);
+    if (grp >= g1 || h >= R.heads) return nullptr;
+    const uint16_t* src = (const uint16_t*)R.in + t * R.in_tok + h * R.in_head;
+    xA = *reinterpret_cast<const uint4*>(src + 8 * pA);
+    xB = *reinterpret_cast<const uint4*>(src + 8 * pB);
+    return (uint16_t*)R.out + t * R.out_tok + h * R.out_head;
   };
-  // the first rows are on their way while the angles of the CTA's tokens are made
-  load(hw & ~1);
-  for (int i = threadIdx.x; i < tn * pairs; i += kRopeThreads) {
-    const int t = i / pairs, f = i % pairs;
-    const double turn = (double)a.pos[t0 + t] * (double)a.inv_freq[f] * 0.15915494309189533577;
-    float s, c;
-    sincospif(2.0f * (float)(turn - rint(turn)), &s, &c);
-    cs[t][f] = make_float2(c, s);
+  uint4 xA, xB;
+  uint16_t* dst = load(g0, xA, xB);
+
+  unsigned long long co[4], si[4];  // of this lane's eight pairs
+  if (a.rot && g0 < nq + nk) {
+    const double pos = (double)a.pos[t];
+    for (int f = lane; f < a.rot / 2; f += 32) {
+      const double turn = pos * (double)a.inv_freq[f] * 0.15915494309189533577;
+      float s, k;
+      sincospif(2.0f * (float)(turn - rint(turn)), &s, &k);
+      table[warp][0][f] = k;
+      table[warp][1][f] = s;
+    }
+    __syncwarp();
+    if (turns) {
+      const ulonglong2* tc = reinterpret_cast<const ulonglong2*>(&table[warp][0][8 * c]);
+      const ulonglong2* ts = reinterpret_cast<const ulonglong2*>(&table[warp][1][8 * c]);
+      co[0] = tc[0].x; co[1] = tc[0].y; co[2] = tc[1].x; co[3] = tc[1].y;
+      si[0] = ts[0].x; si[1] = ts[0].y; si[2] = ts[1].x; si[3] = ts[1].y;
+    }
   }
-  __syncthreads();
-  // both halves of a warp run the same number of rounds (the sums shuffle across the warp)
-  for (int r0 = hw & ~1; r0 < nrows; r0 += kRopeRows * kRopeBatch) {
-    if (r0 != (hw & ~1)) load(r0);
+
+  for (int grp = g0; grp < g1; ++grp) {
+    if (grp > g0) dst = load(grp, xA, xB);
+    if (grp < nq + nk) {  // the same for the whole warp
+      const void* weight = grp < nq ? a.rows[0].weight : a.rows[1].weight;
+      unsigned long long y[8];  // 16 channels: piece A, then piece B
+      y[0] = widen2<BF16>(xA.x); y[1] = widen2<BF16>(xA.y); y[2] = widen2<BF16>(xA.z); y[3] = widen2<BF16>(xA.w);
+      y[4] = widen2<BF16>(xB.x); y[5] = widen2<BF16>(xB.y); y[6] = widen2<BF16>(xB.z); y[7] = widen2<BF16>(xB.w);
+      if (weight) {
+        unsigned long long ss2 = mul2(y[0], y[0]);
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
-      const bool rot = kind[i] < 2;
-      float2 p[4] = {to_f2<BF16>(x[i][0].x), to_f2<BF16>(x[i][0].y), to_f2<BF16>(x[i][1].x), to_f2<BF16>(x[i][1].y)};
-      float ss = 0.f;
+        for (int e = 1; e < 8; ++e) ss2 = fma2(y[e], y[e], ss2);
+        float s0, s1;
+        upk(ss2, s0, s1);
+        float ss = s0 + s1;
+        ss += __shfl_xor_sync(kFull, ss, 4);
+        ss += __shfl_xor_sync(kFull, ss, 2);
+        ss += __shfl_xor_sync(kFull, ss, 1);
+        const float inv = rsqrtf(fmaf(ss, 1.0f / kD, a.eps));
+        const unsigned long long inv2 = pk(inv, inv);
+        const uint4 wA = __ldg(reinterpret_cast<const uint4*>((const uint16_t*)weight + 8 * pA));
+        const uint4 wB = __ldg(reinterpret_cast<const uint4*>((const uint16_t*)weight + 8 * pB));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ss = fmaf(p[e].x, p[e].x, fmaf(p[e].y, p[e].y, ss));
+        for (int e = 0; e < 4; ++e) {
+          y[e] = mul2(mul2(y[e], inv2), widen2<BF16>((&wA.x)[e]));
+          y[e + 4] = mul2(mul2(y[e + 4], inv2), widen2<BF16>((&wB.x)[e]));
+        }
+      }
+      if (turns) {
+        if constexpr (INTER) {  // (u, v) sits in one pair: pair p turns by angle p
 #pragma unroll
-      for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-      if (rot) {
-        if (a.rows[kind[i]].weight) {
-          const float inv = rsqrtf(ss * (1.0f / kD) + a.eps);
-          const uint2* w = kind[i] == 0 ? wq : wk;
-          const float2 f[4] = {to_f2<BF16>(w[0].x), to_f2<BF16>(w[0].y), to_f2<BF16>(w[1].x), to_f2<BF16>(w[1].y)};
+          for (int p = 0; p < 8; ++p) {
+            float u, v, c0, c1, s0, s1;
+            upk(y[p], u, v);
+            upk(co[p / 2], c0, c1);
+            upk(si[p / 2], s0, s1);
+            const float cc = p & 1 ? c1 : c0, s = p & 1 ? s1 : s0;
+            y[p] = fma2(pk(u, v), pk(cc, cc), mul2(pk(v, u), pk(-s, s)));
+          }
+        } else {
+          const unsigned long long minus = pk(-1.0f, -1.0f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            p[e].x = p[e].x * inv * f[e].x;
-            p[e].y = p[e].y * inv * f[e].y;
+            const unsigned long long u = y[e], v = y[e + 4];
+            y[e] = fma2(u, co[e], mul2(mul2(v, si[e]), minus));
+            y[e + 4] = fma2(v, co[e], mul2(u, si[e]));
           }
         }
-        if (turns) {
-          const float4 c01 = *reinterpret_cast<const float4*>(&cs[at[i]][4 * lane16]);
-          const float4 c23 = *reinterpret_cast<const float4*>(&cs[at[i]][4 * lane16 + 2]);
-          const float co[4] = {c01.x, c01.z, c23.x, c23.z}, si[4] = {c01.y, c01.w, c23.y, c23.w};
-          if constexpr (INTER) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              p[e] = make_float2(p[e].x * co[e] - p[e].y * si[e], p[e].y * co[e] + p[e].x * si[e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 u = p[e], v = p[e + 2];
-              p[e] = make_float2(u.x * co[2 * e] - v.x * si[2 * e], u.y * co[2 * e + 1] - v.y * si[2 * e + 1]);
-              p[e + 2] = make_float2(v.x * co[2 * e] + u.x * si[2 * e], v.y * co[2 * e + 1] + u.y * si[2 * e + 1]);
-            }
-          }
-        }
-        x[i][0] = make_uint2(from_f2<BF16>(p[0].x, p[0].y), from_f2<BF16>(p[1].x, p[1].y));
-        x[i][1] = make_uint2(from_f2<BF16>(p[2].x, p[2].y), from_f2<BF16>(p[3].x, p[3].y));
       }
-      if (kind[i] < 3) {
-        *reinterpret_cast<uint2*>(dst[i] + 4 * gA) = x[i][0];
-        *reinterpret_cast<uint2*>(dst[i] + 4 * gB) = x[i][1];
-      }
+      xA = make_uint4(narrow2<BF16>(y[0]), narrow2<BF16>(y[1]), narrow2<BF16>(y[2]), narrow2<BF16>(y[3]));
+      xB = make_uint4(narrow2<BF16>(y[4]), narrow2<BF16>(y[5]), narrow2<BF16>(y[6]), narrow2<BF16>(y[7]));
+    }
+    if (dst) {
+      *reinterpret_cast<uint4*>(dst + 8 * pA) = xA;
+      *reinterpret_cast<uint4*>(dst + 8 * pB) = xB;
     }
   }
 }
@@ -154,13 +155,16 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(RopeArgs a) {
 
 cudaError_t launch_norm_rope(const RopeArgs& a0, int dtype, bool interleaved, int num_sms, cudaStream_t st) {
   RopeArgs a = a0;
-  // a tile of tokens shares its angles; with few tokens every token gets a CTA of its own
-  a.tile = a.tokens >= (int64_t)kRopeTile * num_sms * 4 ? kRopeTile : 1;
-  const int64_t grid = (a.tokens + a.tile - 1) / a.tile;
+  // With many tokens a warp takes all groups of its token; with few, the groups are dealt to more
+  // warps (each makes the token's angles again), down to one group each.
+  const int64_t groups = (a.rows[0].heads + 3) / 4 + (a.rows[1].heads + 3) / 4 + (a.rows[2].heads + 3) / 4;
+  const int64_t warps = (int64_t)num_sms * 32;
+  a.parts = (int)std::min(groups, std::max<int64_t>(1, warps / a.tokens));
+  const int64_t grid = (a.tokens * a.parts + kRopeWarps - 1) / kRopeWarps;
   const bool bf = dtype == KVQ_BF16;
   auto* k = bf ? (interleaved ? norm_rope_kernel<true, true> : norm_rope_kernel<true, false>)
                : (interleaved ? norm_rope_kernel<false, true> : norm_rope_kernel<false, false>);
-  k<<<(unsigned)grid, kRopeThreads, 0, st>>>(a);
+  k<<<(unsigned)grid, kRopeWarps * 32, 0, st>>>(a);
   return cudaGetLastError();
 }
 
