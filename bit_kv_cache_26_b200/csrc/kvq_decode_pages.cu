@@ -19,8 +19,9 @@
 // and KVQ_DEV_RANGE is set.
 //
 // The newest incomplete page takes its keys from the K tail, exact 16-bit operands of the same
-// products.  W is summed without atomics: lanes whose tokens share a pattern take turns in token
-// order, so results do not depend on timing.
+// products.  W is summed in fixed point by integer atomics (2^-19 of the largest weight a warp has
+// met; at most 2048 tokens per warp, so no overflow): whole numbers, so the order does not matter
+// and results do not depend on timing.
 #include <algorithm>
 #include <atomic>
 
@@ -34,7 +35,9 @@ namespace {
 
 constexpr int kStages = 2;   // ring stages per warp
 constexpr int kNW = 4;       // warps per CTA
-constexpr int kPexRow = 36;  // padded row of the p exchange (floats)
+constexpr int kWarpEntries = 64;  // most list entries of a warp (the fixed-point sums hold 2048 tokens)
+constexpr int kWBits = 19;
+constexpr int kQRow = kD + 4;     // row of the query in natural order, its halves 4 floats apart (no bank conflict)
 constexpr float kVFac = 64.0f;  // p s is scaled by it before fp16
 
 template <int BITS>
@@ -74,42 +77,67 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// fp16 pair of the hi parts of v (its fp32 values cut to 11 significant bits) or, on lanes of a lo
-// column, of the remainders: lo_sel = (0, 0) and sign 0 for hi, (1, 1) and the sign bit for lo.
-__device__ __forceinline__ uint32_t split16(unsigned long long v, unsigned long long lo_sel, uint32_t sign) {
-  float v0, v1, r0, r1;
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+  return h;
+}
+// The hi parts of two fp32 values (cut to 11 significant bits) or, on lanes of a lo column, the
+// remainders: lo_sel = (0, 0) and sign 0 for hi, (1, 1) and the sign bit for lo.
+__device__ __forceinline__ void split2(unsigned long long v, unsigned long long lo_sel, uint32_t sign, float (&r)[2]) {
+  float v0, v1;
   upk(v, v0, v1);
   const float t0 = __uint_as_float((__float_as_uint(v0) & 0xFFFFE000u) ^ sign);
   const float t1 = __uint_as_float((__float_as_uint(v1) & 0xFFFFE000u) ^ sign);
-  upk(fma2(lo_sel, v, pk(t0, t1)), r0, r1);
-  uint32_t h;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(r1), "f"(r0));
-  return h;
+  upk(fma2(lo_sel, v, pk(t0, t1)), r[0], r[1]);
+}
+__device__ __forceinline__ uint32_t split16(unsigned long long v, unsigned long long lo_sel, uint32_t sign) {
+  float r[2];
+  split2(v, lo_sel, sign, r);
+  return half2_of(r[0], r[1]);
 }
 
 struct PagesSmem {
-  int bars, qk, qinv, T, W, pex, total;
+  int bars, qk, qinv, T, W, total;
 };
 __host__ __device__ inline PagesSmem pages_smem(int sub_bytes, int NT, int P) {
   PagesSmem s;
   const int NH = NT * 4;
   // the ring; the merge at the end reuses its place
-  const int merge = (kNW * NH * kD + 2 * kNW * NH + kNW * NH * 4 + P * NH + NH * kNW) * 4;
+  const int merge = (kNW * NH * kD + 3 * kNW * NH + kNW * NH * 4 + P * NH + NH * kNW + NH * kD + NH) * 4;
   int o = max(kNW * kStages * sub_bytes, merge);
   o = (o + 15) & ~15;
   s.bars = o; o += kNW * kStages * 8;
   s.qk = o; o += NH * kD * 4;                // query in the quantized space, scaled, KSC order
   s.qinv = o; o += NH * 4;                   // its inverse power of two per head
   s.T = o; o += NH * P * 4;                  // T[head][j], scaled as the query
-  s.W = o; o += kNW * NH * (P + 1) * 4;      // per-warp pattern weights (+1: tokens stored raw)
   o = (o + 15) & ~15;
-  s.pex = o; o += kNW * NH * kPexRow * 4;    // per-warp p exchange
+  s.W = o; o += max(kNW * NH * (P + 1), NH * kQRow) * 4;  // per-warp pattern weights (+1: tokens stored raw); first the query
   s.total = o;
   return s;
 }
 
+// Output of one query head from its channels lane + 32 k of sum p v and its sum p.
+__device__ __forceinline__ void finish_head(const Geom& g, float (&o)[4], float l, const float* vcol, uint16_t* out, int lane) {
+  const float inv = 1.0f / l;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] *= inv;
+  if (g.tx) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] *= vcol[lane + 32 * k];
+    fwht_warp(o, lane);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] *= 0.0078125f;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (!isfinite(o[k])) set_status(g.status, KVQ_DEV_RANGE);
+    out[lane + 32 * k] = g.dtype == KVQ_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(o[k])) : __half_as_ushort(__float2half_rn(o[k]));
+  }
+}
+
 template <int BITS, int NT>
-__global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArgs a) {
+__global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decode_pages_kernel(Geom g, PagesArgs a) {
   constexpr int NH = NT * 4, WPL = BITS * 4;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -124,9 +152,9 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
   float* qk = reinterpret_cast<float*>(smem + sp.qk);
   float* qinv = reinterpret_cast<float*>(smem + sp.qinv);
   float* T = reinterpret_cast<float*>(smem + sp.T);
-  float* Wall = reinterpret_cast<float*>(smem + sp.W);
-  float* Ww = Wall + warp * NH * P1;
-  float* pex = reinterpret_cast<float*>(smem + sp.pex) + warp * NH * kPexRow;
+  int* Wall = reinterpret_cast<int*>(smem + sp.W);
+  int* Ww = Wall + warp * NH * P1;
+  float* qn = reinterpret_cast<float*>(smem + sp.W);  // query in natural order, until T is made
   const unsigned long long lo_sel = (gq & 1) ? pk(1.f, 1.f) : 0ull;
   const uint32_t lo_sign = (gq & 1) ? 0x80000000u : 0u;
 
@@ -220,38 +248,38 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
       for (int k = 0; k < 4; ++k) {
         const int ch = lane + 32 * k;
         qk[hh * kD + ksc_pos(ch)] = v[k] * f * ((ch & 8) ? 1.0f / Code<BITS>::kCol : 1.0f);
-      }
-    }
-    for (int i = threadIdx.x; i < kNW * NH * P1; i += blockDim.x) Wall[i] = 0.f;
-    __syncthreads();
-    for (int hg = 0; hg < NT; ++hg) {
-      float qv[4][4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          qv[x][e] = qk[(4 * hg + x) * kD + ksc_pos(4 * lane + e)] * ((4 * lane & 8) ? Code<BITS>::kCol : 1.0f);
-      for (int j0 = warp; j0 < Pe; j0 += 8 * kNW) {
-        float4 m4[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int j = j0 + u * kNW;
-          m4[u] = j < Pe ? __ldg(reinterpret_cast<const float4*>(MK + (size_t)j * kD) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int j = j0 + u * kNW;
-          float t[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            t[x] = fmaf(qv[x][3], m4[u].w, fmaf(qv[x][2], m4[u].z, fmaf(qv[x][1], m4[u].y, qv[x][0] * m4[u].x)));
-            t[x] = warp_sum(t[x]);
-          }
-          if (lane < 4 && j < Pe) T[(4 * hg + lane) * P + j] = lane == 0 ? t[0] : lane == 1 ? t[1] : lane == 2 ? t[2] : t[3];
-        }
+        qn[hh * kQRow + ch + (ch >= 64 ? 4 : 0)] = v[k] * f;
       }
     }
     __syncthreads();
+    // T: two threads per pattern, half the channels each
+    for (int j0 = 0; j0 < Pe; j0 += kNW * 16) {
+      const int j = j0 + (threadIdx.x >> 1), half = threadIdx.x & 1;
+      const float4* row = reinterpret_cast<const float4*>(MK + (size_t)min(j, Pe - 1) * kD + 64 * half);
+      float4 m[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) m[c] = __ldg(row + c);
+#pragma unroll 4
+      for (int hh = 0; hh < NH; ++hh) {
+        const float4* qr = reinterpret_cast<const float4*>(qn + hh * kQRow + 68 * half);
+        unsigned long long s0 = 0ull, s1 = 0ull;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float4 x = qr[c];
+          s0 = fma2(pk(x.x, x.y), pk(m[c].x, m[c].y), s0);
+          s1 = fma2(pk(x.z, x.w), pk(m[c].z, m[c].w), s1);
+        }
+        float x0, x1, x2, x3;
+        upk(s0, x0, x1);
+        upk(s1, x2, x3);
+        float s = (x0 + x1) + (x2 + x3);
+        s += __shfl_xor_sync(kFull, s, 1);
+        if (half == 0 && j < Pe) T[hh * P + j] = s;
+      }
+    }
+    __syncthreads();
+    for (int i = lane; i < NH * P1; i += 32) Ww[i] = 0;
+    __syncwarp();
 
     // ---- per-thread state (head of tile j: 4 j + tig)
     float accv[NT][8][4], zacc[NT][4], mrun[NT], lrun[NT], scl[NT];
@@ -268,6 +296,7 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
         for (int u = 0; u < 4; ++u) accv[j][mt][u] = 0.f;
     }
 
+    int vexp = g.tx ? -100 : 0;  // pattern weights are in units of 2^(vexp - kWBits): vexp grows with the row factors
     int stuck_at = -1;
     for (int i = 0; i < my_n; ++i) {
       const int st = i % kStages;
@@ -293,39 +322,47 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
             const float4 kr = *reinterpret_cast<const float4*>(pgp + g.off_krow + gq * 16);
             krow[0] = kr.x; krow[1] = kr.y; krow[2] = kr.z; krow[3] = kr.w;
           }
+          float acc[NT][2][4];
+          unsigned long long za2[NT], zb2[NT];
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            unsigned long long za2 = 0ull, zb2 = 0ull;
+            za2[j] = zb2[j] = 0ull;
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-              const float4 s4 = ks4[ks * 4], z4 = kz4[ks * 4];
+            for (int x = 0; x < 8; ++x) acc[j][x >> 2][x & 3] = 0.f;
+          }
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const float4 s4 = ks4[ks * 4], z4 = kz4[ks * 4];
+            uint32_t f[2][4];
+            frag16<BITS>(BITS == 2 ? kw[ks / 2] : kw[ks], ks & 1, f[0]);
+            frag16<BITS>(BITS == 2 ? kw[4 + ks / 2] : kw[8 + ks], ks & 1, f[1]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
               const float4 q4 = reinterpret_cast<const float4*>(qk + (4 * j + (gq >> 1)) * kD)[ks * 4 + tig];
               const unsigned long long qa = pk(q4.x, q4.y), qb = pk(q4.z, q4.w);
-              za2 = fma2(qa, pk(z4.x, z4.y), za2);
-              zb2 = fma2(qb, pk(z4.z, z4.w), zb2);
+              za2[j] = fma2(qa, pk(z4.x, z4.y), za2[j]);
+              zb2[j] = fma2(qb, pk(z4.z, z4.w), zb2[j]);
               const uint32_t b0 = split16(mul2(qa, pk(s4.x, s4.y)), lo_sel, lo_sign);
               const uint32_t b1 = split16(mul2(qb, pk(s4.z, s4.w)), lo_sel, lo_sign);
-#pragma unroll
-              for (int mt = 0; mt < 2; ++mt) {
-                uint32_t f[4];
-                frag16<BITS>(BITS == 2 ? kw[mt * 4 + ks / 2] : kw[mt * 8 + ks], ks & 1, f);
-                mma_f16(acc[mt], f, b0, b1);
-              }
+              mma_f16(acc[j][0], f[0], b0, b1);
+              mma_f16(acc[j][1], f[1], b0, b1);
             }
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
             // zero term of head 4 j + gq / 2: over the 4 tig lanes, then to the lanes of head 4 j + tig
             float z0, z1, z2, z3;
-            upk(za2, z0, z1);
-            upk(zb2, z2, z3);
+            upk(za2[j], z0, z1);
+            upk(zb2[j], z2, z3);
             float zk = fmaf(z2 + z3, Code<BITS>::kCol, z0 + z1);
             zk += __shfl_xor_sync(kFull, zk, 1);
             zk += __shfl_xor_sync(kFull, zk, 2);
             zk = __shfl_sync(kFull, zk, 8 * tig);
             constexpr float f0 = 16777216.0f, f8 = 16777216.0f / Code<BITS>::kRow;
-            sc[j][0] = fmaf(acc[0][0] + acc[0][1], f0, zk);
-            sc[j][1] = fmaf(acc[0][2] + acc[0][3], f8, zk);
-            sc[j][2] = fmaf(acc[1][0] + acc[1][1], f0, zk);
-            sc[j][3] = fmaf(acc[1][2] + acc[1][3], f8, zk);
+            sc[j][0] = fmaf(acc[j][0][0] + acc[j][0][1], f0, zk);
+            sc[j][1] = fmaf(acc[j][0][2] + acc[j][0][3], f8, zk);
+            sc[j][2] = fmaf(acc[j][1][0] + acc[j][1][1], f0, zk);
+            sc[j][3] = fmaf(acc[j][1][2] + acc[j][1][3], f8, zk);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const int idx = min((int)((kidx4 >> (8 * u)) & 0xff), Pe - 1);
@@ -383,18 +420,22 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
         }
         const float4* vz4 = reinterpret_cast<const float4*>(pgp + g.off_vz) + gq;
         const float4 vz[4] = {vz4[0], vz4[8], vz4[16], vz4[24]};
-        // turn of this lane among the lanes of the same head whose token u has the same pattern
-        int vi[4], turn[4], turns = 0;
+        int vi[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          vi[u] = min((int)((vidx4 >> (8 * u)) & 0xff), P);
-          const unsigned same = __match_any_sync(kFull, vi[u]) & (0x11111111u << tig);
-          turn[u] = __popc(same & ((1u << lane) - 1u));
-          turns = max(turns, turn[u]);
+        for (int u = 0; u < 4; ++u) vi[u] = min((int)((vidx4 >> (8 * u)) & 0xff), P);
+        float wscale = (float)(1 << kWBits), wshrink = 1.0f;
+        if (g.tx) {  // the row factors' running power of two
+          const float most = fmaxf(fmaxf(vrow[0], vrow[1]), fmaxf(vrow[2], vrow[3]));
+          const int e = max(-100, min(100, (int)(__reduce_max_sync(kFull, __float_as_uint(most)) >> 23 & 0xff) - 126));
+          if (e > vexp) {
+            wshrink = __uint_as_float((uint32_t)max(0, 127 + vexp - e) << 23);
+            vexp = e;
+          }
+          wscale = __uint_as_float((uint32_t)(127 + kWBits - vexp) << 23);
         }
-        turns = __reduce_max_sync(kFull, (unsigned)turns);
 
         // ---- online softmax (base 2), per head 4 j + tig over the 32 tokens
+        float pa[NT][4], pb[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const int hh = 4 * j + tig;
@@ -406,7 +447,7 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
           const float mnew = fmaxf(mrun[j], pm);
           const float msafe = mnew == -INFINITY ? 0.f : mnew;
           const float alpha = ex2(mrun[j] - msafe);
-          if (__any_sync(kFull, alpha != 1.0f)) {
+          if (__any_sync(kFull, alpha * wshrink != 1.0f)) {
             lrun[j] *= alpha;
 #pragma unroll
             for (int u = 0; u < 4; ++u) zacc[j][u] *= alpha;
@@ -414,7 +455,7 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
             for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
               for (int u = 0; u < 4; ++u) accv[j][mt][u] *= alpha;
-            for (int jj = gq; jj < Pe; jj += 8) Ww[hh * P1 + jj] *= alpha;
+            for (int jj = gq; jj < Pe; jj += 8) Ww[hh * P1 + jj] = __float2int_rn((float)Ww[hh * P1 + jj] * (alpha * wshrink));
             __syncwarp();
           }
           mrun[j] = mnew;
@@ -429,17 +470,20 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
             zacc[j][2] = fmaf(pv[u], vz[u].z, zacc[j][2]);
             zacc[j][3] = fmaf(pv[u], vz[u].w, zacc[j][3]);
           }
-          // tokens 8..15 of each 16 are columns with a factor of their own
-          constexpr float f0 = kVFac, f8 = kVFac / Code<BITS>::kCol;
-          *reinterpret_cast<float4*>(pex + hh * kPexRow + gq * 4) = make_float4(pv[0] * f0, pv[1] * f8, pv[2] * f0, pv[3] * f8);
+          if (real) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            for (int r = 0; r <= turns; ++r) {
-              if (turn[u] == r) Ww[hh * P1 + vi[u]] += pv[u];
-              __syncwarp();
-            }
+            for (int u = 0; u < 4; ++u)  // rounded to whole units by the addition of 1.5 * 2^23
+              atomicAdd(&Ww[hh * P1 + vi[u]], __float_as_int(fmaf(pv[u], wscale, 12582912.0f)) - 0x4B400000);
+          }
+          // p of the B columns of this lane (head 4 j + gq / 2, tokens 2 tig and 2 tig + 1 of each 8), scaled;
+          // tokens 8..15 of each 16 are columns with a factor of their own
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float x = pv[u] * (u & 1 ? kVFac / Code<BITS>::kCol : kVFac);
+            pa[j][u] = __shfl_sync(kFull, x, 8 * tig + (gq >> 1));
+            pb[j][u] = __shfl_sync(kFull, x, 8 * tig + 4 + (gq >> 1));
+          }
         }
-        __syncwarp();
 
         // ---- V: p-weighted codes
         uint32_t vw[WPL];
@@ -450,26 +494,30 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
         }
         const float4* vs4 = reinterpret_cast<const float4*>(pgp + g.off_vs) + tig;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const float* prow = pex + (4 * j + (gq >> 1)) * kPexRow;
-          const float4 pa = *reinterpret_cast<const float4*>(prow + (2 * tig) * 4);
-          const float4 pb = *reinterpret_cast<const float4*>(prow + (2 * tig + 1) * 4);
+        for (int ks = 0; ks < 2; ++ks) {
+          const float4 s0 = vs4[(ks * 4 + 0) * 4], s1 = vs4[(ks * 4 + 1) * 4], s2 = vs4[(ks * 4 + 2) * 4],
+                       s3 = vs4[(ks * 4 + 3) * 4];
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            const unsigned long long p01 = ks ? pk(pa.z, pb.z) : pk(pa.x, pb.x);
-            const unsigned long long p23 = ks ? pk(pa.w, pb.w) : pk(pa.y, pb.y);
-            const float4 s0 = vs4[(ks * 4 + 0) * 4], s1 = vs4[(ks * 4 + 1) * 4], s2 = vs4[(ks * 4 + 2) * 4],
-                         s3 = vs4[(ks * 4 + 3) * 4];
+          for (int j = 0; j < NT; ++j) {
+            const unsigned long long p0 = pk(pa[j][2 * ks], pa[j][2 * ks]), p1 = pk(pb[j][2 * ks], pb[j][2 * ks]);
+            const unsigned long long p2 = pk(pa[j][2 * ks + 1], pa[j][2 * ks + 1]), p3 = pk(pb[j][2 * ks + 1], pb[j][2 * ks + 1]);
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-              const uint32_t b0 = split16(mul2(p01, pk((&s0.x)[q4], (&s1.x)[q4])), lo_sel, lo_sign);
-              const uint32_t b1 = split16(mul2(p23, pk((&s2.x)[q4], (&s3.x)[q4])), lo_sel, lo_sign);
+            for (int gp = 0; gp < 2; ++gp) {  // two channel groups at a time: their scales are neighbours
+              float r0[2], r1[2], r2[2], r3[2];
+              split2(mul2(p0, gp ? pk(s0.z, s0.w) : pk(s0.x, s0.y)), lo_sel, lo_sign, r0);
+              split2(mul2(p1, gp ? pk(s1.z, s1.w) : pk(s1.x, s1.y)), lo_sel, lo_sign, r1);
+              split2(mul2(p2, gp ? pk(s2.z, s2.w) : pk(s2.x, s2.y)), lo_sel, lo_sign, r2);
+              split2(mul2(p3, gp ? pk(s3.z, s3.w) : pk(s3.x, s3.y)), lo_sel, lo_sign, r3);
 #pragma unroll
-              for (int mh = 0; mh < 2; ++mh) {
-                const int mt = q4 * 2 + mh;
-                uint32_t f[4];
-                frag16<BITS>(BITS == 2 ? vw[mt] : vw[mt * 2 + ks], ks, f);
-                mma_f16(accv[j][mt], f, b0, b1);
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t b0 = half2_of(r0[x], r1[x]), b1 = half2_of(r2[x], r3[x]);
+#pragma unroll
+                for (int mh = 0; mh < 2; ++mh) {
+                  const int mt = (2 * gp + x) * 2 + mh;
+                  uint32_t f[4];
+                  frag16<BITS>(BITS == 2 ? vw[mt] : vw[mt * 2 + ks], ks, f);
+                  mma_f16(accv[j][mt], f, b0, b1);
+                }
               }
             }
           }
@@ -511,8 +559,10 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
     float* mm = mo + kNW * NH * kD;              // [kNW][NH] max
     float* ml = mm + kNW * NH;                   // [kNW][NH] sum
     float* mz = ml + kNW * NH;                   // [kNW][NH][4]
-    float* wc = mz + kNW * NH * 4;               // [P][NH] merged pattern weights
+    float* munit = mz + kNW * NH * 4;            // [kNW][NH] unit of the pattern weights
+    float* wc = munit + kNW * NH;                // [P][NH] merged pattern weights
     float* fsh = wc + P * NH;                    // [NH][kNW] warp weights
+    float* ol = fsh + NH * kNW;                  // [NH][128] sum p v, then [NH] sum p (one split)
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int hh = 4 * j + tig;
@@ -525,6 +575,7 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
       if (gq == 0) {
         mm[warp * NH + hh] = mrun[j];
         ml[warp * NH + hh] = lrun[j];
+        munit[warp * NH + hh] = __uint_as_float((uint32_t)(127 - kWBits + vexp) << 23);
 #pragma unroll
         for (int u = 0; u < 4; ++u) mz[(warp * NH + hh) * 4 + u] = zacc[j][u];
       }
@@ -540,11 +591,14 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
         Ls += f[w] * ml[w * NH + hh];
         if (lane == w) fsh[hh * kNW + w] = f[w];
       }
-      if (lane == 0) reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(M, Ls);
+      if (lane == 0) {
+        if (a.nsplit > 1) reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(M, Ls);
+        else ol[NH * kD + hh] = M == -INFINITY ? 0.f : Ls;
+      }
       for (int jj = lane; jj < Pe; jj += 32) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kNW; ++w) s += f[w] * Wall[(w * NH + hh) * P1 + jj];
+        for (int w = 0; w < kNW; ++w) s = fmaf(f[w] * munit[w * NH + hh], (float)Wall[(w * NH + hh) * P1 + jj], s);
         wc[jj * NH + hh] = s;
       }
     }
@@ -556,7 +610,7 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
       float o[NH];
 #pragma unroll
       for (int i = 0; i < NH; ++i) o[i] = 0.f;
-#pragma unroll 8
+#pragma unroll 16
       for (int j = 0; j < Pe; ++j) {
         const float m = __ldg(mv + (size_t)j * kD);
 #pragma unroll
@@ -568,9 +622,24 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
 #pragma unroll
         for (int w = 0; w < kNW; ++w)
           o[i] = fmaf(fsh[i * kNW + w], mo[(w * NH + i) * kD + c] + mz[(w * NH + i) * 4 + (c >> 5)], o[i]);
-        a.part_o[(row0 + (int64_t)i * a.nsplit) * kD + c] = o[i];
+        if (a.nsplit > 1) a.part_o[(row0 + (int64_t)i * a.nsplit) * kD + c] = o[i];
+        else ol[i * kD + c] = o[i];
       }
     }
+    if (a.nsplit == 1) {  // the only split: straight to the output
+      __syncthreads();
+      for (int hh = warp; hh < Gq; hh += kNW) {
+        float o[4], l = ol[NH * kD + hh];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = l == 0.f ? 0.f : ol[hh * kD + lane + 32 * k];
+        finish_head(g, o, l == 0.f ? 1.f : l, g.vcol + sh * kD, a.out + ((int64_t)b * a.Hq + (int64_t)h * Gq + hh) * kD, lane);
+      }
+      return;
+    }
+  } else if (a.nsplit == 1) {  // no entries
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + ((int64_t)b * a.Hq + (int64_t)h * Gq) * kD);
+    for (int i = threadIdx.x; i < Gq * kD / 2; i += blockDim.x) out[i] = 0u;
+    return;
   } else {
     // nothing of the list falls to this CTA
     for (int hh = threadIdx.x; hh < Gq; hh += blockDim.x)
@@ -613,22 +682,8 @@ __global__ void __launch_bounds__(kNW * 32) decode_pages_kernel(Geom g, PagesArg
         }
       }
       Ls = warp_sum(Ls);
-      const float inv = 1.0f / Ls;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] *= inv;
-      if (g.tx) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] *= g.vcol[sh * kD + lane + 32 * k];
-        fwht_warp(o, lane);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] *= 0.0078125f;
-      }
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (!isfinite(o[k])) set_status(g.status, KVQ_DEV_RANGE);
-      outp[lane + 32 * k] = g.dtype == KVQ_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(o[k])) : __half_as_ushort(__float2half_rn(o[k]));
-    }
+    finish_head(g, o, M > -INFINITY ? Ls : 1.f, g.vcol + sh * kD, outp, lane);
   }
 }
 
@@ -653,10 +708,12 @@ cudaError_t launch_bits(const Geom& g, const PagesArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Splits of the list: four CTAs per SM, each with 8 entries or more (two per warp).
+// Splits of the list: four CTAs per SM, each with 8 entries or more (two per warp) and at most
+// kWarpEntries per warp.
 int decode_pages_splits(const Geom& g, int budget, int num_sms) {
   const int64_t units = std::max<int64_t>(1, (int64_t)g.B * g.H), most = std::max(1, budget / 8);
-  return (int)std::min<int64_t>(most, std::max<int64_t>(1, (4 * (int64_t)num_sms + units - 1) / units));
+  const int64_t least = ((int64_t)budget + kNW * kWarpEntries - 1) / (kNW * kWarpEntries);
+  return (int)std::max(least, std::min<int64_t>(most, std::max<int64_t>(1, (4 * (int64_t)num_sms + units - 1) / units)));
 }
 
 static size_t counters_bytes(const Geom& g) { return ((size_t)g.B * g.H * sizeof(int) + 255) / 256 * 256; }
