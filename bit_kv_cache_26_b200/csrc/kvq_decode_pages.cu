@@ -14,16 +14,20 @@
 // half word (S <= 6, so it fits the ten mantissa bits), which the tensor cores multiply exactly.
 // One AND per pair of codes; the powers of two of the four fields of a 16x16 tile separate into a
 // row factor (undone on the sums) and a column factor (folded into B).  B is q s or p s in fp16
-// hi + lo parts (22 bits; columns = query head x {hi, lo}), from a query scaled by a power of two
-// to [16, 32): scales up to 2000 for K and 1000 for V fit fp16; past them the output is not finite
-// and KVQ_DEV_RANGE is set.
+// hi + lo parts (22 bits), from a query scaled by a power of two to [16, 32): scales up to 2000 for K
+// and 1000 for V fit fp16; past them the output is not finite and KVQ_DEV_RANGE is set.
+//
+// Up to four query heads per KV head: the eight columns of a product are (head, {hi, lo}).  The two
+// lanes of a head's columns each form the products of half the channels (tokens for V) and give each
+// other the part the other's column needs: half the shared-memory reads, which were what bounded the
+// loop (68 % of the shared-memory pipe at 67 % of the copy bandwidth).  More heads: the columns are
+// eight heads, and a second product adds the lo parts.
 //
 // The newest incomplete page takes its keys from the K tail, exact 16-bit operands of the same
 // products.  W is summed in fixed point by integer atomics (2^-19 of the largest weight a warp has
 // met; at most 2048 tokens per warp, so no overflow): whole numbers, so the order does not matter
 // and results do not depend on timing.
 #include <algorithm>
-#include <atomic>
 
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
@@ -37,8 +41,10 @@ constexpr int kStages = 2;   // ring stages per warp
 constexpr int kNW = 4;       // warps per CTA
 constexpr int kWarpEntries = 64;  // most list entries of a warp (the fixed-point sums hold 2048 tokens)
 constexpr int kWBits = 19;
+constexpr int kMvAhead = 16;      // pattern values in flight per thread in the final sum
 constexpr int kQRow = kD + 4;     // row of the query in natural order, its halves 4 floats apart (no bank conflict)
-constexpr float kVFac = 64.0f;  // p s is scaled by it before fp16
+constexpr int kPexRow = 36;       // padded row of the p exchange (floats)
+constexpr float kVFac = 64.0f;    // p s is scaled by it before fp16
 
 template <int BITS>
 struct Code {
@@ -46,19 +52,20 @@ struct Code {
   static constexpr float kCol = BITS == 2 ? 16.0f : 1.0f;  // factor of columns 8..15
 };
 
-// The A registers of tile half `odd` of word w (2-bit: two tiles per word; 4-bit: one).
+// The A registers of tile half `odd` of word w (2-bit: two tiles per word; 4-bit: one); `swapped`: with the
+// two columns of each register exchanged.
 template <int BITS>
-__device__ __forceinline__ void frag16(uint32_t w, int odd, uint32_t (&a)[4]) {
+__device__ __forceinline__ void frag16(uint32_t w, int odd, uint32_t (&a)[4], bool swapped = false) {
   if constexpr (BITS == 2) {
-    if (odd) w >>= 8;
-    a[0] = w & 0x00030003u;
-    a[1] = w & 0x000C000Cu;
-    a[2] = w & 0x00300030u;
-    a[3] = w & 0x00C000C0u;
+    const uint32_t x = swapped ? __funnelshift_r(w, w, odd ? 24 : 16) : odd ? w >> 8 : w;
+    a[0] = x & 0x00030003u;
+    a[1] = x & 0x000C000Cu;
+    a[2] = x & 0x00300030u;
+    a[3] = x & 0x00C000C0u;
   } else {
-    const uint32_t y = w >> 8;
-    a[0] = w & 0x000F000Fu;
-    a[1] = w & 0x00F000F0u;
+    const uint32_t x = swapped ? __funnelshift_r(w, w, 16) : w, y = swapped ? __funnelshift_r(w, w, 24) : w >> 8;
+    a[0] = x & 0x000F000Fu;
+    a[1] = x & 0x00F000F0u;
     a[2] = y & 0x000F000Fu;
     a[3] = y & 0x00F000F0u;
   }
@@ -82,82 +89,115 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
   return h;
 }
-// The hi parts of two fp32 values (cut to 11 significant bits) or, on lanes of a lo column, the
-// remainders: lo_sel = (0, 0) and sign 0 for hi, (1, 1) and the sign bit for lo.
-__device__ __forceinline__ void split2(unsigned long long v, unsigned long long lo_sel, uint32_t sign, float (&r)[2]) {
+// fp16 pairs of the hi parts (11 significant bits) of two fp32 values and of what is left of them.
+__device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  hi = half2_of(v0, v1);
+  const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  lo = half2_of(v0 - t.x, v1 - t.y);
+}
+__device__ __forceinline__ void split2(unsigned long long v, uint32_t& hi, uint32_t& lo) {
   float v0, v1;
   upk(v, v0, v1);
-  const float t0 = __uint_as_float((__float_as_uint(v0) & 0xFFFFE000u) ^ sign);
-  const float t1 = __uint_as_float((__float_as_uint(v1) & 0xFFFFE000u) ^ sign);
-  upk(fma2(lo_sel, v, pk(t0, t1)), r[0], r[1]);
-}
-__device__ __forceinline__ uint32_t split16(unsigned long long v, unsigned long long lo_sel, uint32_t sign) {
-  float r[2];
-  split2(v, lo_sel, sign, r);
-  return half2_of(r[0], r[1]);
+  split2(v0, v1, hi, lo);
 }
 
+// Smallest row stride >= n whose rows start `step` banks apart.
+__host__ __device__ constexpr int banked(int n, int step) { return n + ((step - n) % 32 + 32) % 32; }
+
 struct PagesSmem {
-  int bars, qk, qinv, T, W, total;
+  int bars, qk, qinv, T, W, pex, total;
+  int t_row, w_row;
 };
-__host__ __device__ inline PagesSmem pages_smem(int sub_bytes, int NT, int P) {
+__host__ __device__ inline PagesSmem pages_smem(int sub_bytes, int NT, bool wide, int P) {
   PagesSmem s;
-  const int NH = NT * 4;
+  const int NH = NT * (wide ? 8 : 4);
+  s.t_row = banked(P, wide ? 4 : 8);
+  s.w_row = banked(P + 1, wide ? 4 : 8);  // +1: tokens stored raw
   // the ring; the merge at the end reuses its place
   const int merge = (kNW * NH * kD + 3 * kNW * NH + kNW * NH * 4 + P * NH + NH * kNW + NH * kD + NH) * 4;
   int o = max(kNW * kStages * sub_bytes, merge);
   o = (o + 15) & ~15;
   s.bars = o; o += kNW * kStages * 8;
-  s.qk = o; o += NH * kD * 4;                // query in the quantized space, scaled, KSC order
-  s.qinv = o; o += NH * 4;                   // its inverse power of two per head
-  s.T = o; o += NH * P * 4;                  // T[head][j], scaled as the query
+  s.qinv = o; o += NH * 4;                    // inverse power of two of the query scale per head
+  s.T = o; o += NH * s.t_row * 4;             // T[head][j], scaled as the query
+  s.qk = o; o += wide ? NH * kD * 4 : 0;      // query in the quantized space, scaled, KSC order
+  s.pex = o; o += wide ? kNW * NH * kPexRow * 4 : 0;  // per-warp p exchange
   o = (o + 15) & ~15;
-  s.W = o; o += max(kNW * NH * (P + 1), NH * kQRow) * 4;  // per-warp pattern weights (+1: tokens stored raw); first the query
+  s.W = o;                                    // per-warp pattern weights; first the query in natural order (and in
+  const int first = NH * (kQRow + (wide ? 0 : kD));  // KSC order, when its users then keep it in registers)
+  o += max(kNW * NH * s.w_row, first) * 4;
+  if (!wide) s.qk = s.W + NH * kQRow * 4;
   s.total = o;
   return s;
 }
 
-// Output of one query head from its channels lane + 32 k of sum p v and its sum p.
+// Output of one query head from its channels 4 lane .. 4 lane + 3 of sum p v and its sum p.
 __device__ __forceinline__ void finish_head(const Geom& g, float (&o)[4], float l, const float* vcol, uint16_t* out, int lane) {
   const float inv = 1.0f / l;
 #pragma unroll
   for (int k = 0; k < 4; ++k) o[k] *= inv;
   if (g.tx) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] *= vcol[lane + 32 * k];
-    fwht_warp(o, lane);
+    for (int k = 0; k < 4; ++k) o[k] *= __ldg(vcol + 4 * lane + k);
+    // Walsh-Hadamard: strides 1 and 2 in the lane, 4 .. 64 across lanes
+    float p0 = o[0] + o[1], p1 = o[0] - o[1], p2 = o[2] + o[3], p3 = o[2] - o[3];
+    o[0] = p0 + p2; o[2] = p0 - p2; o[1] = p1 + p3; o[3] = p1 - p3;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float other = __shfl_xor_sync(kFull, o[k], s);
+        o[k] = (lane & s) ? other - o[k] : o[k] + other;
+      }
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[k] *= 0.0078125f;
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (!isfinite(o[k])) set_status(g.status, KVQ_DEV_RANGE);
-    out[lane + 32 * k] = g.dtype == KVQ_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(o[k])) : __half_as_ushort(__float2half_rn(o[k]));
+  if (!(isfinite(o[0]) && isfinite(o[1]) && isfinite(o[2]) && isfinite(o[3]))) set_status(g.status, KVQ_DEV_RANGE);
+  uint2 r;
+  if (g.dtype == KVQ_BF16) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o[0], o[1]), y = __floats2bfloat162_rn(o[2], o[3]);
+    r = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  } else {
+    r = make_uint2(half2_of(o[0], o[1]), half2_of(o[2], o[3]));
   }
+  reinterpret_cast<uint2*>(out)[lane] = r;
 }
 
-template <int BITS, int NT>
-__global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decode_pages_kernel(Geom g, PagesArgs a) {
-  constexpr int NH = NT * 4, WPL = BITS * 4;
+// NT tiles of four query heads (or eight: WIDE).  Thread (gq, tig) of a warp holds the sums of head
+// 4 j + tig of tile j (WIDE: heads 8 j + 2 tig and the next) and forms the B columns of head
+// 4 j + gq / 2 (WIDE: 8 j + gq).
+template <int BITS, int NT, bool WIDE>
+__global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode_pages_kernel(Geom g, PagesArgs a) {
+  static_assert(WIDE || NT == 1, "more than four heads: wide tiles");
+  constexpr int HPT = WIDE ? 2 : 1, TH = 4 * HPT, NH = NT * TH, WPL = BITS * 4;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int gq = lane >> 2, tig = lane & 3;
+  const int gq = lane >> 2, tig = lane & 3, part = gq & 1;
   const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int64_t grp = (int64_t)b * g.H + h;
-  const int Gq = a.Gq, P = g.P, P1 = P + 1;
+  const int Gq = a.Gq, P = g.P;
   const int sub_bytes = (int)g.sub_bytes;
-  const PagesSmem sp = pages_smem(sub_bytes, NT, P);
+  const PagesSmem sp = pages_smem(sub_bytes, NT, WIDE, P);
+  const int TR = sp.t_row, WR = sp.w_row;
   uint8_t* ring = smem + warp * kStages * sub_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + sp.bars) + warp * kStages;
   float* qk = reinterpret_cast<float*>(smem + sp.qk);
   float* qinv = reinterpret_cast<float*>(smem + sp.qinv);
   float* T = reinterpret_cast<float*>(smem + sp.T);
   int* Wall = reinterpret_cast<int*>(smem + sp.W);
-  int* Ww = Wall + warp * NH * P1;
+  int* Ww = Wall + warp * NH * WR;
   float* qn = reinterpret_cast<float*>(smem + sp.W);  // query in natural order, until T is made
-  const unsigned long long lo_sel = (gq & 1) ? pk(1.f, 1.f) : 0ull;
-  const uint32_t lo_sign = (gq & 1) ? 0x80000000u : 0u;
+  float* pex = reinterpret_cast<float*>(smem + sp.pex) + warp * NH * kPexRow;
 
+  // entries of this warp: split + nsplit (warp + kNW i).  Lane l of window w reads entry i = 32 w + l; the first
+  // window goes out with the lengths.
+  const int32_t* list = a.list + grp * a.budget;
+  const int stride = a.nsplit * kNW, e_first = split + a.nsplit * warp;
+  auto entry = [&](int i) -> int {
+    const int64_t e = e_first + (int64_t)stride * i;
+    return e < a.budget ? __ldg(list + e) : -1;
+  };
+  int lp = entry(lane);
   int L = g.seq_len[b];
   int n_list = a.list_len[grp];
   const bool teller = threadIdx.x == 0 && split == 0;
@@ -176,24 +216,38 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
     n_list = 0;
   }
   const int nfull = L / kG, ntail = L % kG, npages = nfull + (ntail > 0);
-  const int per = (n_list + a.nsplit - 1) / a.nsplit;
-  const int e0 = min(n_list, split * per), e1 = min(n_list, e0 + per);
+  // this CTA's entries: split, split + nsplit, ... (dealt so that the list can be read before its length is known)
+  const int n_mine = (n_list - split + a.nsplit - 1) / a.nsplit;
   const size_t sh = (size_t)set * g.H + h;
   const int Pe = p_eff(g, (int)sh);
   const float* MK = g.kpat + sh * P * kD;
   const int64_t row0 = ((int64_t)b * a.Hq + (int64_t)h * Gq) * a.nsplit + split;  // partial row of head 0; + hh * nsplit
 
-  if (e0 < e1) {
-    // entries of this warp: e0 + warp + kNW * i.  Lane l of window w holds entry 32 w + l: the physical
-    // page, -1 where the entry names none, and whether it is the newest incomplete page.
-    const int my_n = (e1 - e0 - warp + kNW - 1) / kNW;
-    const int32_t* list = a.list + grp * a.budget + e0 + warp;
+  if (n_mine > 0) {
+    // the first of the setup's loads go out before the page copies, which would keep them waiting: this warp's
+    // query row and this thread's half of a pattern row
+    uint16_t q_raw[4];
+    auto load_q = [&](int hh) {
+      const uint16_t* src = a.q + ((int64_t)b * a.Hq + (int64_t)h * Gq + min(hh, Gq - 1)) * kD + lane;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q_raw[k] = __ldg(src + 32 * k);
+    };
+    const int half = threadIdx.x & 1;
+    float4 m[16];
+    auto load_pattern = [&](int j) {
+      const float4* row = reinterpret_cast<const float4*>(MK + (size_t)min(j, Pe - 1) * kD + 64 * half);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) m[c] = __ldg(row + c);
+    };
+    load_q(warp);
+    load_pattern(threadIdx.x >> 1);
+    // the physical page of this lane's entry, -1 where it names none; whether it is the newest incomplete page
+    const int my_n = (n_mine - warp + kNW - 1) / kNW;
     unsigned tails = 0;
     auto load_ids = [&](int base) -> int {
-      const int i = base + lane;
-      int phys = -1, lp = -1;
-      if (i < my_n) {
-        lp = list[kNW * i];
+      if (base > 0) lp = entry(base + lane);
+      int phys = -1;
+      if (base + lane < my_n) {
         if (lp >= 0 && lp < npages) phys = g.page_table[(int64_t)b * g.maxp + lp];
         if (phys < 0 || phys >= g.npages) {
           set_status(g.status, KVQ_DEV_BAD_PAGE);
@@ -229,9 +283,9 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
     // ---- queries, T, zeroed W (over the first copies)
     for (int hh = warp; hh < NH; hh += kNW) {
       float v[4], m = 0.f;
-      const uint16_t* src = a.q + ((int64_t)b * a.Hq + (int64_t)h * Gq + min(hh, Gq - 1)) * kD;
+      if (hh > warp) load_q(hh);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = hh < Gq ? load_elem(src + lane + 32 * k, g.dtype) : 0.f;
+      for (int k = 0; k < 4; ++k) v[k] = hh < Gq ? bits_to_float(q_raw[k], g.dtype) : 0.f;
       if (g.tx) {
         fwht_warp(v, lane);
 #pragma unroll
@@ -254,11 +308,8 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
     __syncthreads();
     // T: two threads per pattern, half the channels each
     for (int j0 = 0; j0 < Pe; j0 += kNW * 16) {
-      const int j = j0 + (threadIdx.x >> 1), half = threadIdx.x & 1;
-      const float4* row = reinterpret_cast<const float4*>(MK + (size_t)min(j, Pe - 1) * kD + 64 * half);
-      float4 m[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) m[c] = __ldg(row + c);
+      const int j = j0 + (threadIdx.x >> 1);
+      if (j0 > 0) load_pattern(j);
 #pragma unroll 4
       for (int hh = 0; hh < NH; ++hh) {
         const float4* qr = reinterpret_cast<const float4*>(qn + hh * kQRow + 68 * half);
@@ -274,22 +325,31 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
         upk(s1, x2, x3);
         float s = (x0 + x1) + (x2 + x3);
         s += __shfl_xor_sync(kFull, s, 1);
-        if (half == 0 && j < Pe) T[hh * P + j] = s;
+        if (half == 0 && j < Pe) T[hh * TR + j] = s;
       }
     }
+    // the query of this lane's columns: narrow tiles keep the half they need in registers
+    float4 qreg[4];
+    if constexpr (!WIDE) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) qreg[c] = reinterpret_cast<const float4*>(qk + (gq >> 1) * kD)[(2 * c + part) * 4 + tig];
+    }
     __syncthreads();
-    for (int i = lane; i < NH * P1; i += 32) Ww[i] = 0;
+    for (int i = lane; i < NH * WR; i += 32) Ww[i] = 0;
     __syncwarp();
 
-    // ---- per-thread state (head of tile j: 4 j + tig)
-    float accv[NT][8][4], zacc[NT][4], mrun[NT], lrun[NT], scl[NT];
+    // ---- per-thread state
+    float accv[NT][8][4], zacc[NT][HPT][4], mrun[NT][HPT], lrun[NT][HPT], scl[NT][HPT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      mrun[j] = -INFINITY;
-      lrun[j] = 0.f;
-      scl[j] = a.scale_log2 * qinv[4 * j + tig];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) zacc[j][u] = 0.f;
+      for (int x = 0; x < HPT; ++x) {
+        mrun[j][x] = -INFINITY;
+        lrun[j][x] = 0.f;
+        scl[j][x] = a.scale_log2 * qinv[TH * j + HPT * tig + x];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) zacc[j][x][u] = 0.f;
+      }
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
@@ -305,7 +365,7 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
       uint8_t* pgp = ring + st * sub_bytes;
       if (!(skips >> st & 1)) {
         const bool tail = tail_st >> st & 1;
-        float sc[NT][4];
+        float sc[NT][HPT][4];  // token gq + 8 u
         if (!tail) {
           // ---- K: scores of the page's 32 tokens
           uint32_t kw[WPL];
@@ -322,7 +382,7 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
             const float4 kr = *reinterpret_cast<const float4*>(pgp + g.off_krow + gq * 16);
             krow[0] = kr.x; krow[1] = kr.y; krow[2] = kr.z; krow[3] = kr.w;
           }
-          float acc[NT][2][4];
+          float acc[NT][2][4], zk[NT];
           unsigned long long za2[NT], zb2[NT];
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
@@ -330,66 +390,93 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
 #pragma unroll
             for (int x = 0; x < 8; ++x) acc[j][x >> 2][x & 3] = 0.f;
           }
+          if constexpr (!WIDE) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const float4 s4 = ks4[ks * 4], z4 = kz4[ks * 4];
-            uint32_t f[2][4];
-            frag16<BITS>(BITS == 2 ? kw[ks / 2] : kw[ks], ks & 1, f[0]);
-            frag16<BITS>(BITS == 2 ? kw[4 + ks / 2] : kw[8 + ks], ks & 1, f[1]);
+            for (int c = 0; c < 4; ++c) {  // of channel steps 2 c and 2 c + 1, one is this lane's, the other its partner's
+              const float4 s4 = ks4[(2 * c + part) * 4], z4 = kz4[(2 * c + part) * 4];
+              const unsigned long long qa = pk(qreg[c].x, qreg[c].y), qb = pk(qreg[c].z, qreg[c].w);
+              za2[0] = fma2(qa, pk(z4.x, z4.y), za2[0]);
+              zb2[0] = fma2(qb, pk(z4.z, z4.w), zb2[0]);
+              uint32_t own0, own1, lo0, lo1;
+              split2(mul2(qa, pk(s4.x, s4.y)), own0, lo0);
+              split2(mul2(qb, pk(s4.z, s4.w)), own1, lo1);
+              const uint32_t got0 = __shfl_xor_sync(kFull, lo0, 4), got1 = __shfl_xor_sync(kFull, lo1, 4);
+              // (which of the two columns holds hi and which lo is the other way round in the odd steps: they are added)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const float4 q4 = reinterpret_cast<const float4*>(qk + (4 * j + (gq >> 1)) * kD)[ks * 4 + tig];
-              const unsigned long long qa = pk(q4.x, q4.y), qb = pk(q4.z, q4.w);
-              za2[j] = fma2(qa, pk(z4.x, z4.y), za2[j]);
-              zb2[j] = fma2(qb, pk(z4.z, z4.w), zb2[j]);
-              const uint32_t b0 = split16(mul2(qa, pk(s4.x, s4.y)), lo_sel, lo_sign);
-              const uint32_t b1 = split16(mul2(qb, pk(s4.z, s4.w)), lo_sel, lo_sign);
-              mma_f16(acc[j][0], f[0], b0, b1);
-              mma_f16(acc[j][1], f[1], b0, b1);
+              for (int s = 0; s < 2; ++s) {
+                const int ks = 2 * c + s;
+                const uint32_t b0 = part == s ? own0 : got0, b1 = part == s ? own1 : got1;
+                uint32_t f[4];
+                frag16<BITS>(BITS == 2 ? kw[ks / 2] : kw[ks], ks & 1, f);
+                mma_f16(acc[0][0], f, b0, b1);
+                frag16<BITS>(BITS == 2 ? kw[4 + ks / 2] : kw[8 + ks], ks & 1, f);
+                mma_f16(acc[0][1], f, b0, b1);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              const float4 s4 = ks4[ks * 4], z4 = kz4[ks * 4];
+              uint32_t f[2][4];
+              frag16<BITS>(BITS == 2 ? kw[ks / 2] : kw[ks], ks & 1, f[0]);
+              frag16<BITS>(BITS == 2 ? kw[4 + ks / 2] : kw[8 + ks], ks & 1, f[1]);
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+                const float4 q4 = reinterpret_cast<const float4*>(qk + (TH * j + gq) * kD)[ks * 4 + tig];
+                const unsigned long long qa = pk(q4.x, q4.y), qb = pk(q4.z, q4.w);
+                za2[j] = fma2(qa, pk(z4.x, z4.y), za2[j]);
+                zb2[j] = fma2(qb, pk(z4.z, z4.w), zb2[j]);
+                uint32_t bh0, bh1, bl0, bl1;
+                split2(mul2(qa, pk(s4.x, s4.y)), bh0, bl0);
+                split2(mul2(qb, pk(s4.z, s4.w)), bh1, bl1);
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                  mma_f16(acc[j][mt], f[mt], bh0, bh1);
+                  mma_f16(acc[j][mt], f[mt], bl0, bl1);
+                }
+              }
             }
           }
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            // zero term of head 4 j + gq / 2: over the 4 tig lanes, then to the lanes of head 4 j + tig
+            // zero term of this lane's column, summed over the lanes that share it
             float z0, z1, z2, z3;
             upk(za2[j], z0, z1);
             upk(zb2[j], z2, z3);
-            float zk = fmaf(z2 + z3, Code<BITS>::kCol, z0 + z1);
-            zk += __shfl_xor_sync(kFull, zk, 1);
-            zk += __shfl_xor_sync(kFull, zk, 2);
-            zk = __shfl_sync(kFull, zk, 8 * tig);
-            constexpr float f0 = 16777216.0f, f8 = 16777216.0f / Code<BITS>::kRow;
-            sc[j][0] = fmaf(acc[j][0][0] + acc[j][0][1], f0, zk);
-            sc[j][1] = fmaf(acc[j][0][2] + acc[j][0][3], f8, zk);
-            sc[j][2] = fmaf(acc[j][1][0] + acc[j][1][1], f0, zk);
-            sc[j][3] = fmaf(acc[j][1][2] + acc[j][1][3], f8, zk);
+            zk[j] = fmaf(z2 + z3, Code<BITS>::kCol, z0 + z1);
+            zk[j] += __shfl_xor_sync(kFull, zk[j], 1);
+            zk[j] += __shfl_xor_sync(kFull, zk[j], 2);
+            if constexpr (!WIDE) zk[j] += __shfl_xor_sync(kFull, zk[j], 4);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int idx = min((int)((kidx4 >> (8 * u)) & 0xff), Pe - 1);
-              sc[j][u] = (sc[j][u] + T[(4 * j + tig) * P + idx]) * (krow[u] * scl[j]);
+            for (int x = 0; x < HPT; ++x) {
+              const float z = __shfl_sync(kFull, zk[j], WIDE ? 4 * (2 * tig + x) : 8 * tig);
+              constexpr float f0 = 16777216.0f, f8 = 16777216.0f / Code<BITS>::kRow;
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float s = WIDE ? acc[j][u >> 1][2 * (u & 1) + x] : acc[j][u >> 1][2 * (u & 1)] + acc[j][u >> 1][2 * (u & 1) + 1];
+                const int idx = min((int)((kidx4 >> (8 * u)) & 0xff), Pe - 1);
+                sc[j][x][u] = (fmaf(s, u & 1 ? f8 : f0, z) + T[(TH * j + HPT * tig + x) * TR + idx]) * (krow[u] * scl[j][x]);
+              }
             }
           }
         } else {
           // ---- K tail: exact keys; tokens that are not there yet score -inf and store nothing of V
           const uint16_t* kt = g.k_tail + grp * kG * kD;
-          {
-            const int t = lane;
-            if (t >= ntail) {
+          if (lane >= ntail) {
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                reinterpret_cast<float*>(pgp + g.off_vs)[vsc_pos(t, u)] = 0.f;
-                reinterpret_cast<float*>(pgp + g.off_vz)[vzc_pos(t, u)] = 0.f;
-              }
-              pgp[g.off_vidx + tok_pos(t)] = (uint8_t)kRawIndex;
-              if (g.tx) reinterpret_cast<float*>(pgp + g.off_vrow)[tok_pos(t)] = 0.f;
+            for (int u = 0; u < 4; ++u) {
+              reinterpret_cast<float*>(pgp + g.off_vs)[vsc_pos(lane, u)] = 0.f;
+              reinterpret_cast<float*>(pgp + g.off_vz)[vzc_pos(lane, u)] = 0.f;
             }
-            __syncwarp();
+            pgp[g.off_vidx + tok_pos(lane)] = (uint8_t)kRawIndex;
+            if (g.tx) reinterpret_cast<float*>(pgp + g.off_vrow)[tok_pos(lane)] = 0.f;
           }
+          __syncwarp();
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            const int hq = 4 * j + (gq >> 1);
-            const bool has = hq < Gq && !(gq & 1);
+            const int hq = TH * j + (WIDE ? gq : gq >> 1);
+            const bool has = hq < Gq && (WIDE || part == 0);
             const uint16_t* qr = a.q + ((int64_t)b * a.Hq + (int64_t)h * Gq + min(hq, Gq - 1)) * kD + 2 * tig;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
@@ -408,8 +495,10 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
               }
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              sc[j][u] = gq + 8 * u < ntail ? acc[u >> 1][2 * (u & 1)] * a.scale_log2 : -INFINITY;
+            for (int x = 0; x < HPT; ++x)
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                sc[j][x][u] = gq + 8 * u < ntail ? acc[u >> 1][2 * (u & 1) + x] * a.scale_log2 : -INFINITY;
           }
         }
         const uint32_t vidx4 = *reinterpret_cast<const uint32_t*>(pgp + g.off_vidx + gq * 4);
@@ -434,56 +523,80 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
           wscale = __uint_as_float((uint32_t)(127 + kWBits - vexp) << 23);
         }
 
-        // ---- online softmax (base 2), per head 4 j + tig over the 32 tokens
-        float pa[NT][4], pb[NT][4];
+        // ---- online softmax (base 2), per head over the 32 tokens
+        float p0[4];  // narrow: p of this lane's four V columns' tokens
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const int hh = 4 * j + tig;
-          const bool real = hh < Gq;
-          float pm = fmaxf(fmaxf(sc[j][0], sc[j][1]), fmaxf(sc[j][2], sc[j][3]));
-          pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 4));
-          pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 8));
-          pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 16));
-          const float mnew = fmaxf(mrun[j], pm);
-          const float msafe = mnew == -INFINITY ? 0.f : mnew;
-          const float alpha = ex2(mrun[j] - msafe);
-          if (__any_sync(kFull, alpha * wshrink != 1.0f)) {
-            lrun[j] *= alpha;
+          float mnew[HPT], alpha[HPT];
+          bool same = true;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) zacc[j][u] *= alpha;
+          for (int x = 0; x < HPT; ++x) {
+            float pm = fmaxf(fmaxf(sc[j][x][0], sc[j][x][1]), fmaxf(sc[j][x][2], sc[j][x][3]));
+            pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 4));
+            pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 8));
+            pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 16));
+            const float m = fmaxf(mrun[j][x], pm);
+            mnew[x] = m == -INFINITY ? 0.f : m;
+            alpha[x] = ex2(mrun[j][x] - mnew[x]);
+            mrun[j][x] = m;
+            same = same && alpha[x] * wshrink == 1.0f;
+          }
+          if (!__all_sync(kFull, same)) {
 #pragma unroll
-            for (int mt = 0; mt < 8; ++mt)
+            for (int x = 0; x < HPT; ++x) {
+              const int hh = TH * j + HPT * tig + x;
+              lrun[j][x] *= alpha[x];
 #pragma unroll
-              for (int u = 0; u < 4; ++u) accv[j][mt][u] *= alpha;
-            for (int jj = gq; jj < Pe; jj += 8) Ww[hh * P1 + jj] = __float2int_rn((float)Ww[hh * P1 + jj] * (alpha * wshrink));
+              for (int u = 0; u < 4; ++u) zacc[j][x][u] *= alpha[x];
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  if (!WIDE || (u & 1) == x) accv[j][mt][u] *= alpha[x];
+              for (int jj = gq; jj < Pe; jj += 8)
+                Ww[hh * WR + jj] = __float2int_rn((float)Ww[hh * WR + jj] * (alpha[x] * wshrink));
+            }
             __syncwarp();
           }
-          mrun[j] = mnew;
-          float pv[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float p = real ? ex2(sc[j][u] - msafe) : 0.f;
-            lrun[j] += p;
-            pv[u] = p * vrow[u];
-            zacc[j][0] = fmaf(pv[u], vz[u].x, zacc[j][0]);
-            zacc[j][1] = fmaf(pv[u], vz[u].y, zacc[j][1]);
-            zacc[j][2] = fmaf(pv[u], vz[u].z, zacc[j][2]);
-            zacc[j][3] = fmaf(pv[u], vz[u].w, zacc[j][3]);
-          }
-          if (real) {
+          for (int x = 0; x < HPT; ++x) {
+            const int hh = TH * j + HPT * tig + x;
+            const bool real = hh < Gq;
+            float pv[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)  // rounded to whole units by the addition of 1.5 * 2^23
-              atomicAdd(&Ww[hh * P1 + vi[u]], __float_as_int(fmaf(pv[u], wscale, 12582912.0f)) - 0x4B400000);
-          }
-          // p of the B columns of this lane (head 4 j + gq / 2, tokens 2 tig and 2 tig + 1 of each 8), scaled;
-          // tokens 8..15 of each 16 are columns with a factor of their own
+            for (int u = 0; u < 4; ++u) {
+              const float p = real ? ex2(sc[j][x][u] - mnew[x]) : 0.f;
+              lrun[j][x] += p;
+              pv[u] = p * vrow[u];
+              zacc[j][x][0] = fmaf(pv[u], vz[u].x, zacc[j][x][0]);
+              zacc[j][x][1] = fmaf(pv[u], vz[u].y, zacc[j][x][1]);
+              zacc[j][x][2] = fmaf(pv[u], vz[u].z, zacc[j][x][2]);
+              zacc[j][x][3] = fmaf(pv[u], vz[u].w, zacc[j][x][3]);
+            }
+            if (real) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float x = pv[u] * (u & 1 ? kVFac / Code<BITS>::kCol : kVFac);
-            pa[j][u] = __shfl_sync(kFull, x, 8 * tig + (gq >> 1));
-            pb[j][u] = __shfl_sync(kFull, x, 8 * tig + 4 + (gq >> 1));
+              for (int u = 0; u < 4; ++u)  // rounded to whole units by the addition of 1.5 * 2^23
+                atomicAdd(&Ww[hh * WR + vi[u]], __float_as_int(fmaf(pv[u], wscale, 12582912.0f)) - 0x4B400000);
+            }
+            // p to the lanes of the V columns, scaled; tokens 8..15 of each 16 are columns with a factor of their own
+            constexpr float f0 = kVFac, f8 = kVFac / Code<BITS>::kCol;
+            if constexpr (WIDE) {
+              *reinterpret_cast<float4*>(pex + hh * kPexRow + gq * 4) = make_float4(pv[0] * f0, pv[1] * f8, pv[2] * f0, pv[3] * f8);
+            } else {
+              // Lane (head, part) wants tokens 2 tig and 2 tig + 1 (+ 8) of the page's half `part`: u = 2 part, 2 part + 1.
+              // Even token rows offer the halves in one order, odd rows in the other, so that both exchanges serve both
+              // parts; part 1 gets 2 tig + 1 first (and reads its scales in that order: no bank conflict with part 0).
+              const float y0 = (part ? pv[2] : pv[0]) * f0, y1 = (part ? pv[3] : pv[1]) * f8;
+              const float z0 = (part ? pv[0] : pv[2]) * f0, z1 = (part ? pv[1] : pv[3]) * f8;
+              const int src = 8 * tig + (gq >> 1) + 4 * part;  // row 2 tig + part
+              p0[0] = __shfl_sync(kFull, y0, src);
+              p0[1] = __shfl_sync(kFull, z0, src ^ 4);
+              p0[2] = __shfl_sync(kFull, y1, src);
+              p0[3] = __shfl_sync(kFull, z1, src ^ 4);
+            }
           }
         }
+        if constexpr (WIDE) __syncwarp();
 
         // ---- V: p-weighted codes
         uint32_t vw[WPL];
@@ -493,30 +606,66 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
           vw[4 * c] = t.x; vw[4 * c + 1] = t.y; vw[4 * c + 2] = t.z; vw[4 * c + 3] = t.w;
         }
         const float4* vs4 = reinterpret_cast<const float4*>(pgp + g.off_vs) + tig;
+        if constexpr (!WIDE) {
+          const float4 s0 = vs4[5 * part * 4], s1 = vs4[(3 * part + 1) * 4], s2 = vs4[(5 * part + 2) * 4], s3 = vs4[(3 * part + 3) * 4];
+          const unsigned long long q0 = pk(p0[0], p0[0]), q1 = pk(p0[1], p0[1]), q2 = pk(p0[2], p0[2]), q3 = pk(p0[3], p0[3]);
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const float4 s0 = vs4[(ks * 4 + 0) * 4], s1 = vs4[(ks * 4 + 1) * 4], s2 = vs4[(ks * 4 + 2) * 4],
-                       s3 = vs4[(ks * 4 + 3) * 4];
+          for (int gp = 0; gp < 2; ++gp) {  // two channel groups at a time: their scales are neighbours
+            float v0[2], v1[2], v2[2], v3[2];
+            upk(mul2(q0, gp ? pk(s0.z, s0.w) : pk(s0.x, s0.y)), v0[0], v0[1]);
+            upk(mul2(q1, gp ? pk(s1.z, s1.w) : pk(s1.x, s1.y)), v1[0], v1[1]);
+            upk(mul2(q2, gp ? pk(s2.z, s2.w) : pk(s2.x, s2.y)), v2[0], v2[1]);
+            upk(mul2(q3, gp ? pk(s3.z, s3.w) : pk(s3.x, s3.y)), v3[0], v3[1]);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const unsigned long long p0 = pk(pa[j][2 * ks], pa[j][2 * ks]), p1 = pk(pb[j][2 * ks], pb[j][2 * ks]);
-            const unsigned long long p2 = pk(pa[j][2 * ks + 1], pa[j][2 * ks + 1]), p3 = pk(pb[j][2 * ks + 1], pb[j][2 * ks + 1]);
+            for (int x = 0; x < 2; ++x) {
+              uint32_t own0, own1, lo0, lo1;
+              split2(v0[x], v1[x], own0, lo0);
+              split2(v2[x], v3[x], own1, lo1);
+              const uint32_t got0 = __shfl_xor_sync(kFull, lo0, 4), got1 = __shfl_xor_sync(kFull, lo1, 4);
 #pragma unroll
-            for (int gp = 0; gp < 2; ++gp) {  // two channel groups at a time: their scales are neighbours
-              float r0[2], r1[2], r2[2], r3[2];
-              split2(mul2(p0, gp ? pk(s0.z, s0.w) : pk(s0.x, s0.y)), lo_sel, lo_sign, r0);
-              split2(mul2(p1, gp ? pk(s1.z, s1.w) : pk(s1.x, s1.y)), lo_sel, lo_sign, r1);
-              split2(mul2(p2, gp ? pk(s2.z, s2.w) : pk(s2.x, s2.y)), lo_sel, lo_sign, r2);
-              split2(mul2(p3, gp ? pk(s3.z, s3.w) : pk(s3.x, s3.y)), lo_sel, lo_sign, r3);
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t b0 = half2_of(r0[x], r1[x]), b1 = half2_of(r2[x], r3[x]);
+              for (int ks = 0; ks < 2; ++ks) {
+                const uint32_t b0 = part == ks ? own0 : got0, b1 = part == ks ? own1 : got1;
 #pragma unroll
                 for (int mh = 0; mh < 2; ++mh) {
                   const int mt = (2 * gp + x) * 2 + mh;
                   uint32_t f[4];
-                  frag16<BITS>(BITS == 2 ? vw[mt] : vw[mt * 2 + ks], ks, f);
-                  mma_f16(accv[j][mt], f, b0, b1);
+                  frag16<BITS>(BITS == 2 ? vw[mt] : vw[mt * 2 + ks], ks, f, ks == 1);
+                  mma_f16(accv[0][mt], f, b0, b1);
+                }
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            const float4 s0 = vs4[(ks * 4 + 0) * 4], s1 = vs4[(ks * 4 + 1) * 4], s2 = vs4[(ks * 4 + 2) * 4],
+                         s3 = vs4[(ks * 4 + 3) * 4];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const float* prow = pex + (TH * j + gq) * kPexRow + 2 * ks;
+              const float2 pa = *reinterpret_cast<const float2*>(prow + (2 * tig) * 4);
+              const float2 pb = *reinterpret_cast<const float2*>(prow + (2 * tig + 1) * 4);
+              const unsigned long long q0 = pk(pa.x, pa.x), q1 = pk(pb.x, pb.x), q2 = pk(pa.y, pa.y), q3 = pk(pb.y, pb.y);
+#pragma unroll
+              for (int gp = 0; gp < 2; ++gp) {
+                float v0[2], v1[2], v2[2], v3[2];
+                upk(mul2(q0, gp ? pk(s0.z, s0.w) : pk(s0.x, s0.y)), v0[0], v0[1]);
+                upk(mul2(q1, gp ? pk(s1.z, s1.w) : pk(s1.x, s1.y)), v1[0], v1[1]);
+                upk(mul2(q2, gp ? pk(s2.z, s2.w) : pk(s2.x, s2.y)), v2[0], v2[1]);
+                upk(mul2(q3, gp ? pk(s3.z, s3.w) : pk(s3.x, s3.y)), v3[0], v3[1]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  uint32_t bh0, bh1, bl0, bl1;
+                  split2(v0[x], v1[x], bh0, bl0);
+                  split2(v2[x], v3[x], bh1, bl1);
+#pragma unroll
+                  for (int mh = 0; mh < 2; ++mh) {
+                    const int mt = (2 * gp + x) * 2 + mh;
+                    uint32_t f[4];
+                    frag16<BITS>(BITS == 2 ? vw[mt] : vw[mt * 2 + ks], ks, f);
+                    mma_f16(accv[j][mt], f, bh0, bh1);
+                    mma_f16(accv[j][mt], f, bl0, bl1);
+                  }
                 }
               }
             }
@@ -546,14 +695,15 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
 
     // ---- merge the warps and write the partials
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        lrun[j] += __shfl_xor_sync(kFull, lrun[j], o);
+      for (int x = 0; x < HPT; ++x)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) zacc[j][u] += __shfl_xor_sync(kFull, zacc[j][u], o);
-      }
-    }
+        for (int o = 4; o < 32; o <<= 1) {
+          lrun[j][x] += __shfl_xor_sync(kFull, lrun[j][x], o);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) zacc[j][x][u] += __shfl_xor_sync(kFull, zacc[j][x][u], o);
+        }
     __syncthreads();  // every warp is done with its ring
     float* mo = reinterpret_cast<float*>(smem);  // [kNW][NH][128]
     float* mm = mo + kNW * NH * kD;              // [kNW][NH] max
@@ -564,22 +714,29 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
     float* fsh = wc + P * NH;                    // [NH][kNW] warp weights
     float* ol = fsh + NH * kNW;                  // [NH][128] sum p v, then [NH] sum p (one split)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int hh = 4 * j + tig;
-      constexpr float f0 = 16777216.0f / kVFac, f8 = 16777216.0f / kVFac / Code<BITS>::kRow;
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int mt = 0; mt < 8; ++mt) {
-        mo[(warp * NH + hh) * kD + 16 * mt + gq] = (accv[j][mt][0] + accv[j][mt][1]) * f0;
-        mo[(warp * NH + hh) * kD + 16 * mt + gq + 8] = (accv[j][mt][2] + accv[j][mt][3]) * f8;
-      }
-      if (gq == 0) {
-        mm[warp * NH + hh] = mrun[j];
-        ml[warp * NH + hh] = lrun[j];
-        munit[warp * NH + hh] = __uint_as_float((uint32_t)(127 - kWBits + vexp) << 23);
+      for (int x = 0; x < HPT; ++x) {
+        const int hh = TH * j + HPT * tig + x;
+        constexpr float f0 = 16777216.0f / kVFac, f8 = 16777216.0f / kVFac / Code<BITS>::kRow;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mz[(warp * NH + hh) * 4 + u] = zacc[j][u];
+        for (int mt = 0; mt < 8; ++mt) {
+          mo[(warp * NH + hh) * kD + 16 * mt + gq] = (WIDE ? accv[j][mt][x] : accv[j][mt][0] + accv[j][mt][1]) * f0;
+          mo[(warp * NH + hh) * kD + 16 * mt + gq + 8] = (WIDE ? accv[j][mt][2 + x] : accv[j][mt][2] + accv[j][mt][3]) * f8;
+        }
+        if (gq == 0) {
+          mm[warp * NH + hh] = mrun[j][x];
+          ml[warp * NH + hh] = lrun[j][x];
+          munit[warp * NH + hh] = __uint_as_float((uint32_t)(127 - kWBits + vexp) << 23);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mz[(warp * NH + hh) * 4 + u] = zacc[j][x][u];
+        }
       }
-    }
+    // M_V values of this thread's channel, the first of them over the merge of the weights
+    const float* mv = g.vpat + sh * P * kD + threadIdx.x;
+    float mval[kMvAhead];
+#pragma unroll
+    for (int j = 0; j < kMvAhead; ++j) mval[j] = __ldg(mv + (size_t)min(j, Pe - 1) * kD);
     __syncthreads();
     for (int hh = warp; hh < Gq; hh += kNW) {
       float M = -INFINITY, Ls = 0.f, f[kNW];
@@ -598,7 +755,7 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
       for (int jj = lane; jj < Pe; jj += 32) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kNW; ++w) s = fmaf(f[w] * munit[w * NH + hh], (float)Wall[(w * NH + hh) * P1 + jj], s);
+        for (int w = 0; w < kNW; ++w) s = fmaf(f[w] * munit[w * NH + hh], (float)Wall[(w * NH + hh) * WR + jj], s);
         wc[jj * NH + hh] = s;
       }
     }
@@ -606,15 +763,21 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
     // thread = channel; each M_V value is read once per CTA
     {
       const int c = threadIdx.x;
-      const float* mv = g.vpat + sh * P * kD + c;
       float o[NH];
 #pragma unroll
       for (int i = 0; i < NH; ++i) o[i] = 0.f;
-#pragma unroll 16
-      for (int j = 0; j < Pe; ++j) {
-        const float m = __ldg(mv + (size_t)j * kD);
+      for (int j0 = 0; j0 < Pe; j0 += kMvAhead) {
+        if (j0 > 0) {
 #pragma unroll
-        for (int i = 0; i < NH; ++i) o[i] = fmaf(wc[j * NH + i], m, o[i]);
+          for (int j = 0; j < kMvAhead; ++j) mval[j] = __ldg(mv + (size_t)min(j0 + j, Pe - 1) * kD);
+        }
+#pragma unroll
+        for (int j = 0; j < kMvAhead; ++j) {
+          if (j0 + j < Pe) {
+#pragma unroll
+            for (int i = 0; i < NH; ++i) o[i] = fmaf(wc[(j0 + j) * NH + i], mval[j], o[i]);
+          }
+        }
       }
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
@@ -631,7 +794,7 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
       for (int hh = warp; hh < Gq; hh += kNW) {
         float o[4], l = ol[NH * kD + hh];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = l == 0.f ? 0.f : ol[hh * kD + lane + 32 * k];
+        for (int k = 0; k < 4; ++k) o[k] = l == 0.f ? 0.f : ol[hh * kD + 4 * lane + k];
         finish_head(g, o, l == 0.f ? 1.f : l, g.vcol + sh * kD, a.out + ((int64_t)b * a.Hq + (int64_t)h * Gq + hh) * kD, lane);
       }
       return;
@@ -674,11 +837,15 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
           Ls = fmaf(fs, x.y, Ls);
         }
         const int n = min(32, a.nsplit - s0);
+#pragma unroll 8
         for (int i = 0; i < n; ++i) {
           const float f = __shfl_sync(kFull, fs, i);
-          if (f == 0.f) continue;  // a split without entries has written no row
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = fmaf(f, __ldcg(a.part_o + (base + s0 + i) * kD + lane + 32 * k), o[k]);
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + (base + s0 + i) * kD) + lane);
+          // (a split without entries has written no row: its weight is 0, whatever is read)
+          o[0] += f == 0.f ? 0.f : f * x.x;
+          o[1] += f == 0.f ? 0.f : f * x.y;
+          o[2] += f == 0.f ? 0.f : f * x.z;
+          o[3] += f == 0.f ? 0.f : f * x.w;
         }
       }
       Ls = warp_sum(Ls);
@@ -687,33 +854,47 @@ __global__ void __launch_bounds__(kNW * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) decod
   }
 }
 
-template <int BITS, int NT>
+template <int BITS, int NT, bool WIDE>
 cudaError_t launch_one(const Geom& g, const PagesArgs& a, cudaStream_t st) {
-  const int smem = pages_smem((int)g.sub_bytes, NT, g.P).total;
-  cudaError_t e = cudaFuncSetAttribute(decode_pages_kernel<BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = pages_smem((int)g.sub_bytes, NT, WIDE, g.P).total;
+  cudaError_t e = cudaFuncSetAttribute(decode_pages_kernel<BITS, NT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode_pages_kernel<BITS, NT><<<dim3(a.nsplit, g.H, g.B), kNW * 32, smem, st>>>(g, a);
+  decode_pages_kernel<BITS, NT, WIDE><<<dim3(a.nsplit, g.H, g.B), kNW * 32, smem, st>>>(g, a);
   return cudaGetLastError();
 }
 
 template <int BITS>
 cudaError_t launch_bits(const Geom& g, const PagesArgs& a, cudaStream_t st) {
-  switch ((a.Gq + 3) / 4) {
-    case 1: return launch_one<BITS, 1>(g, a, st);
-    case 2: return launch_one<BITS, 2>(g, a, st);
-    case 3: return launch_one<BITS, 3>(g, a, st);
-    default: return launch_one<BITS, 4>(g, a, st);
-  }
+  if (a.Gq <= 4) return launch_one<BITS, 1, false>(g, a, st);
+  if (a.Gq <= 8) return launch_one<BITS, 1, true>(g, a, st);
+  return launch_one<BITS, 2, true>(g, a, st);
 }
 
 }  // namespace
 
-// Splits of the list: four CTAs per SM, each with 8 entries or more (two per warp) and at most
-// kWarpEntries per warp.
-int decode_pages_splits(const Geom& g, int budget, int num_sms) {
-  const int64_t units = std::max<int64_t>(1, (int64_t)g.B * g.H), most = std::max(1, budget / 8);
-  const int64_t least = ((int64_t)budget + kNW * kWarpEntries - 1) / (kNW * kWarpEntries);
-  return (int)std::max(least, std::min<int64_t>(most, std::max<int64_t>(1, (4 * (int64_t)num_sms + units - 1) / units)));
+// Splits of the list.  Model, in units of the time a lone CTA takes for a page per warp (1.3 us on one B200): k CTAs on an
+// SM at once take max(1, 0.48 k) for a page per warp and 5 + 1.25 (k - 1) before and after the loop; the busiest SM runs
+// its CTAs `occ` at a time; merging costs a little per split.  At most kWarpEntries entries per warp.  Measured at 64
+// listed pages of 4 bits for 8 groups (best 16 splits, 13.7 us; 1: 30 us; 64: 28 us), for 64 groups (best 4), at 256 pages
+// for 8 groups (best 16), at 128 pages for 256 groups (best 2) and 2048 (1).
+int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms) {
+  const int64_t units = std::max<int64_t>(1, (int64_t)g.B * g.H), sms = std::max(1, num_sms);
+  const bool wide = Gq > 4;
+  const int by_regs = !wide ? 4 : Gq <= 8 ? 3 : 2;
+  const int by_smem = 233472 / (pages_smem((int)g.sub_bytes, Gq > 8 ? 2 : 1, wide, g.P).total + 1024 + 128);
+  const int64_t occ = std::max(1, std::min(by_regs, by_smem));
+  const int least = (int)(((int64_t)budget + kNW * kWarpEntries - 1) / (kNW * kWarpEntries));
+  const int most = std::max(least, std::min(64, budget));
+  auto round = [&](int64_t k, int pages) { return 5.0 + 1.25 * (k - 1) + pages * std::max(1.0, 0.48 * k); };
+  int best = least;
+  double best_cost = 1e300;
+  for (int ns = least; ns <= most; ++ns) {
+    const int64_t per_sm = (units * ns + sms - 1) / sms, full = per_sm / occ, rem = per_sm % occ;
+    const int pages = ((budget + ns - 1) / ns + kNW - 1) / kNW;
+    const double cost = full * round(occ, pages) + (rem ? round(rem, pages) : 0.0) + 0.05 * ns;
+    if (cost < best_cost * (1.0 - 1e-9)) { best_cost = cost; best = ns; }
+  }
+  return best;
 }
 
 static size_t counters_bytes(const Geom& g) { return ((size_t)g.B * g.H * sizeof(int) + 255) / 256 * 256; }

@@ -47,7 +47,7 @@ struct PagesArgs {
   float* part_o;
   int* arrivals;
 };
-int decode_pages_splits(const Geom& g, int budget, int num_sms);
+int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms);
 size_t decode_pages_workspace(const Geom& g, int Hq, int nsplit);
 cudaError_t launch_decode_pages(const Geom& g, PagesArgs a, void* ws, cudaStream_t st);
 
