@@ -41,8 +41,7 @@ constexpr int kStages = 2;   // ring stages per warp
 constexpr int kNW = 4;       // warps per CTA
 constexpr int kWarpEntries = 64;  // most list entries of a warp (the fixed-point sums hold 2048 tokens)
 constexpr int kWBits = 19;
-constexpr int kMvAhead = 16;      // pattern values in flight per thread in the final sum
-constexpr int kQRow = kD + 4;     // row of the query in natural order, its halves 4 floats apart (no bank conflict)
+constexpr int kMvAhead = 64;      // pattern values in flight per thread in the final sum
 constexpr int kPexRow = 36;       // padded row of the p exchange (floats)
 constexpr float kVFac = 64.0f;    // p s is scaled by it before fp16
 
@@ -124,9 +123,9 @@ __host__ __device__ inline PagesSmem pages_smem(int sub_bytes, int NT, bool wide
   s.pex = o; o += wide ? kNW * NH * kPexRow * 4 : 0;  // per-warp p exchange
   o = (o + 15) & ~15;
   s.W = o;                                    // per-warp pattern weights; first the query in natural order (and in
-  const int first = NH * (kQRow + (wide ? 0 : kD));  // KSC order, when its users then keep it in registers)
+  const int first = NH * (kD + (wide ? 0 : kD));  // KSC order, when its users then keep it in registers)
   o += max(kNW * NH * s.w_row, first) * 4;
-  if (!wide) s.qk = s.W + NH * kQRow * 4;
+  if (!wide) s.qk = s.W + NH * kD * 4;
   s.total = o;
   return s;
 }
@@ -225,22 +224,25 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 
   if (n_mine > 0) {
     // the first of the setup's loads go out before the page copies, which would keep them waiting: this warp's
-    // query row and this thread's half of a pattern row
+    // query row and this thread's quarters of two pattern rows (four lanes per row, 16 bytes in turn)
     uint16_t q_raw[4];
     auto load_q = [&](int hh) {
       const uint16_t* src = a.q + ((int64_t)b * a.Hq + (int64_t)h * Gq + min(hh, Gq - 1)) * kD + lane;
 #pragma unroll
       for (int k = 0; k < 4; ++k) q_raw[k] = __ldg(src + 32 * k);
     };
-    const int half = threadIdx.x & 1;
-    float4 m[16];
-    auto load_pattern = [&](int j) {
-      const float4* row = reinterpret_cast<const float4*>(MK + (size_t)min(j, Pe - 1) * kD + 64 * half);
+    const int quarter = threadIdx.x & 3;
+    float4 m[2][8];
+    auto load_patterns = [&](int j) {
 #pragma unroll
-      for (int c = 0; c < 16; ++c) m[c] = __ldg(row + c);
+      for (int r = 0; r < 2; ++r) {
+        const float4* row = reinterpret_cast<const float4*>(MK + (size_t)min(j + 32 * r, Pe - 1) * kD) + quarter;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) m[r][c] = __ldg(row + 4 * c);
+      }
     };
     load_q(warp);
-    load_pattern(threadIdx.x >> 1);
+    load_patterns(threadIdx.x >> 2);
     // the physical page of this lane's entry, -1 where it names none; whether it is the newest incomplete page
     const int my_n = (n_mine - warp + kNW - 1) / kNW;
     unsigned tails = 0;
@@ -302,30 +304,38 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
       for (int k = 0; k < 4; ++k) {
         const int ch = lane + 32 * k;
         qk[hh * kD + ksc_pos(ch)] = v[k] * f * ((ch & 8) ? 1.0f / Code<BITS>::kCol : 1.0f);
-        qn[hh * kQRow + ch + (ch >= 64 ? 4 : 0)] = v[k] * f;
+        qn[hh * kD + ch] = v[k] * f;
       }
     }
     __syncthreads();
-    // T: two threads per pattern, half the channels each
-    for (int j0 = 0; j0 < Pe; j0 += kNW * 16) {
-      const int j = j0 + (threadIdx.x >> 1);
-      if (j0 > 0) load_pattern(j);
+    // T: four lanes per pattern, two patterns at a time
+    static_assert(kNW * 32 == 4 * 32, "32 rows per round and half");
+    for (int j0 = 0; j0 < Pe; j0 += 64) {
+      const int j = j0 + (threadIdx.x >> 2);
+      if (j0 > 0) load_patterns(j);
 #pragma unroll 4
       for (int hh = 0; hh < NH; ++hh) {
-        const float4* qr = reinterpret_cast<const float4*>(qn + hh * kQRow + 68 * half);
-        unsigned long long s0 = 0ull, s1 = 0ull;
+        const float4* qr = reinterpret_cast<const float4*>(qn + hh * kD) + quarter;
+        unsigned long long s[2][2] = {{0ull, 0ull}, {0ull, 0ull}};
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float4 x = qr[c];
-          s0 = fma2(pk(x.x, x.y), pk(m[c].x, m[c].y), s0);
-          s1 = fma2(pk(x.z, x.w), pk(m[c].z, m[c].w), s1);
+        for (int c = 0; c < 8; ++c) {
+          const float4 x = qr[4 * c];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            s[r][0] = fma2(pk(x.x, x.y), pk(m[r][c].x, m[r][c].y), s[r][0]);
+            s[r][1] = fma2(pk(x.z, x.w), pk(m[r][c].z, m[r][c].w), s[r][1]);
+          }
         }
-        float x0, x1, x2, x3;
-        upk(s0, x0, x1);
-        upk(s1, x2, x3);
-        float s = (x0 + x1) + (x2 + x3);
-        s += __shfl_xor_sync(kFull, s, 1);
-        if (half == 0 && j < Pe) T[hh * TR + j] = s;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float x0, x1, x2, x3;
+          upk(s[r][0], x0, x1);
+          upk(s[r][1], x2, x3);
+          float y = (x0 + x1) + (x2 + x3);
+          y += __shfl_xor_sync(kFull, y, 1);
+          y += __shfl_xor_sync(kFull, y, 2);
+          if (quarter == 0 && j + 32 * r < Pe) T[hh * TR + j + 32 * r] = y;
+        }
       }
     }
     // the query of this lane's columns: narrow tiles keep the half they need in registers
@@ -824,28 +834,32 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
     const int64_t row = (int64_t)b * a.Hq + (int64_t)h * Gq + hh, base = row * a.nsplit;
     uint16_t* outp = a.out + row * kD;
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + base;
-    float M = -INFINITY;
-    for (int s = lane; s < a.nsplit; s += 32) M = fmaxf(M, __ldcg(ml + s).x);
+    float2 x = make_float2(-INFINITY, 0.f);  // of split lane (the first 32)
+    if (lane < a.nsplit) x = __ldcg(ml + lane);
+    float M = x.x;
+    for (int s = 32 + lane; s < a.nsplit; s += 32) M = fmaxf(M, __ldcg(ml + s).x);
     M = warp_max(M);
     float Ls = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
     if (M > -INFINITY) {
       for (int s0 = 0; s0 < a.nsplit; s0 += 32) {
-        float fs = 0.f;
-        if (s0 + lane < a.nsplit) {
-          const float2 x = __ldcg(ml + s0 + lane);
-          fs = x.x == -INFINITY ? 0.f : ex2(x.x - M);
-          Ls = fmaf(fs, x.y, Ls);
-        }
+        if (s0 > 0) x = s0 + lane < a.nsplit ? __ldcg(ml + s0 + lane) : make_float2(-INFINITY, 0.f);
+        const float fs = x.x == -INFINITY ? 0.f : ex2(x.x - M);
+        Ls = fmaf(fs, x.y, Ls);
         const int n = min(32, a.nsplit - s0);
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-          const float f = __shfl_sync(kFull, fs, i);
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + (base + s0 + i) * kD) + lane);
-          // (a split without entries has written no row: its weight is 0, whatever is read)
-          o[0] += f == 0.f ? 0.f : f * x.x;
-          o[1] += f == 0.f ? 0.f : f * x.y;
-          o[2] += f == 0.f ? 0.f : f * x.z;
-          o[3] += f == 0.f ? 0.f : f * x.w;
+        for (int i0 = 0; i0 < n; i0 += 8) {
+          float4 y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            y[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (base + min(s0 + i0 + i, a.nsplit - 1)) * kD) + lane);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            // (a split without entries has written no row: its weight is 0, whatever is read; so past the last one)
+            const float f = __shfl_sync(kFull, fs, i0 + i);
+            o[0] += f == 0.f ? 0.f : f * y[i].x;
+            o[1] += f == 0.f ? 0.f : f * y[i].y;
+            o[2] += f == 0.f ? 0.f : f * y[i].z;
+            o[3] += f == 0.f ? 0.f : f * y[i].w;
+          }
         }
       }
       Ls = warp_sum(Ls);
