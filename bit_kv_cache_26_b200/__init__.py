@@ -216,9 +216,9 @@ def _want(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int
 
 def _here(stream) -> tuple[int, int]:
     """The current device and the stream to use (the current one unless given)."""
-    if not torch.cuda.is_available():  # no tensor can be on a device then: the checks that follow say so
+    if not torch.cuda.is_initialized():  # no tensor can be on a device then: the checks that follow say so
         return 0, 0
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     return dev, _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
@@ -465,7 +465,7 @@ class PagedKVCache:
     # -- the rest of a serving step ------------------------------------------------------------
 
     def plan_workspace(self) -> torch.Tensor:
-        return _alloc_aligned(max(256, kvq_plan_workspace_bytes(self.c)), self.device)
+        return _alloc_aligned(max(256, kvq_plan_workspace_bytes(self.c)), self.device, zero=True)
 
     def plan(self, new_len: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor, cu_new: torch.Tensor,
              slot_map: torch.Tensor, positions: torch.Tensor, seq_ids: torch.Tensor, ws: torch.Tensor, stream=None) -> None:

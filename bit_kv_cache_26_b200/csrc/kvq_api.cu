@@ -1,6 +1,7 @@
 // C-ABI entry points of libkvq (declared in include/kvq.h): host-side argument
 // validation, workspace sizing and kernel launches.  No exception crosses the
 // ABI; nothing here allocates device memory.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -29,9 +30,14 @@ kvq_status cuda_fail(cudaError_t e, const char* where) {
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 int num_sms() {
+  static std::atomic<int> known[64];  // per device, asked once
   int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms > 0 ? sms : 148;
+  if (cudaGetDevice(&dev) != cudaSuccess) return sms;
+  const bool kept = dev >= 0 && dev < 64;
+  if (kept && known[dev].load(std::memory_order_relaxed) > 0) return known[dev].load(std::memory_order_relaxed);
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 148;
+  if (kept) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
 }
 
 kvq_status check_cache(const kvq_cache* c) {

@@ -28,6 +28,7 @@
 // met; at most 2048 tokens per warp, so no overflow): whole numbers, so the order does not matter
 // and results do not depend on timing.
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
@@ -42,6 +43,7 @@ constexpr int kNW = 4;       // warps per CTA
 constexpr int kWarpEntries = 64;  // most list entries of a warp (the fixed-point sums hold 2048 tokens)
 constexpr int kWBits = 19;
 constexpr int kMvAhead = 64;      // pattern values in flight per thread in the final sum
+constexpr int kMaxSmem = 200 * 1024;  // dynamic, of a CTA (the largest shape, 255 patterns and 16 heads a group, takes 157 KB)
 constexpr int kPexRow = 36;       // padded row of the p exchange (floats)
 constexpr float kVFac = 64.0f;    // p s is scaled by it before fp16
 
@@ -871,8 +873,16 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 template <int BITS, int NT, bool WIDE>
 cudaError_t launch_one(const Geom& g, const PagesArgs& a, cudaStream_t st) {
   const int smem = pages_smem((int)g.sub_bytes, NT, WIDE, g.P).total;
-  cudaError_t e = cudaFuncSetAttribute(decode_pages_kernel<BITS, NT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the kernel's shared-memory limit is raised when a call first needs more on this device
+  static std::atomic<int> allowed[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || allowed[dev].load(std::memory_order_relaxed) < smem) {
+    e = cudaFuncSetAttribute(decode_pages_kernel<BITS, NT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) allowed[dev].store(kMaxSmem, std::memory_order_relaxed);
+  }
   decode_pages_kernel<BITS, NT, WIDE><<<dim3(a.nsplit, g.H, g.B), kNW * 32, smem, st>>>(g, a);
   return cudaGetLastError();
 }

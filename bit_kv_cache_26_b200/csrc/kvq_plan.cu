@@ -5,6 +5,8 @@
 // in the packed order and every new page its place on the free stack, whose top is taken first.
 // A sequence is served when the scans up to and including it stay within the slot map and the
 // stack; both scans only grow, so the served ones are those before the first that does not fit.
+#include <algorithm>
+
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
 
@@ -12,10 +14,11 @@ namespace kvq {
 
 namespace {
 
-constexpr int kPlanScan = 1024;       // threads of the scan
-constexpr int kPlanThreads = 256;     // threads of an expanding CTA
-constexpr int kPlanChunk = 4096;      // tokens of an expanding CTA
-constexpr int64_t kPlanOneCta = 4096; // up to so many tokens the scanning CTA expands them itself
+constexpr int kPlanThreads = 256;
+constexpr int kPlanOnce = 2048;       // up to so many sequences every CTA makes the scans for itself: one launch
+constexpr int kPlanItems = kPlanOnce / kPlanThreads;
+constexpr int64_t kOnceTokens = 1 << 19;  // and so many tokens (512 CTAs: beyond, making the scans once is faster)
+constexpr int kPlanScan = 1024;       // threads of the scan when it is a launch of its own
 
 __device__ __forceinline__ longlong2 add2ll(longlong2 a, longlong2 b) { return make_longlong2(a.x + b.x, a.y + b.y); }
 
@@ -45,24 +48,23 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int i, int lo, int hi) 
   return lo;
 }
 
-// Packed tokens [begin, end) of the plan, four consecutive ones per thread and round.
-__device__ void expand(const Geom& g, const PlanArgs& a, int begin, int end, int s_lo, int s_hi, int free_n, int tid,
-                       int nthreads) {
-  const int32_t* before = a.ws + 4;  // new pages of the sequences before
-  for (int i0 = begin + 4 * tid; i0 < end; i0 += 4 * nthreads) {
-    int s = seq_of(a.cu, i0, s_lo, s_hi), base = -1, next = -1, L = 0, held = 0, page = -1, phys = 0;
-    int pos[4], ids[4];
-    int64_t slot[4];
+// Packed tokens [begin, end) of the plan, two consecutive ones per thread and round (a warp's stores are whole sectors).  cu, before (new pages of the
+// sequences before) and len: in shared or global memory.
+__device__ __forceinline__ void expand(const Geom& g, const PlanArgs& a, const int32_t* cu, const int32_t* before,
+                                       const int32_t* len, int begin, int end, int s_lo, int s_hi, int free_n) {
+  for (int i0 = begin + 2 * (int)threadIdx.x; i0 < end; i0 += 2 * kPlanThreads) {
+    int s = seq_of(cu, i0, s_lo, s_hi), base = -1, next = -1, L = 0, held = 0, page = -1, phys = 0;
+    int pos[2], ids[2];
+    int64_t slot[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 2; ++e) {
       const int i = i0 + e;
       if (i < end) {
         if (i >= next) {
-          if (next >= 0) ++s;
-          while (a.cu[s + 1] <= i) ++s;  // sequences without new tokens
-          base = a.cu[s];
-          next = a.cu[s + 1];
-          L = g.seq_len[s];
+          while (cu[s + 1] <= i) ++s;  // the next sequence with new tokens
+          base = cu[s];
+          next = cu[s + 1];
+          L = len[s];
           held = (L + kG - 1) / kG;
           page = -1;
         }
@@ -77,32 +79,106 @@ __device__ void expand(const Geom& g, const PlanArgs& a, int begin, int end, int
         if (pos[e] % kG == 0) const_cast<int32_t*>(g.page_table)[(int64_t)s * g.maxp + p] = phys;
       }
     }
-    if (i0 + 4 <= end) {
-      *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-      *reinterpret_cast<int4*>(a.seq_ids + i0) = make_int4(ids[0], ids[1], ids[2], ids[3]);
+    if (i0 + 2 <= end) {
+      *reinterpret_cast<int2*>(a.positions + i0) = make_int2(pos[0], pos[1]);
+      *reinterpret_cast<int2*>(a.seq_ids + i0) = make_int2(ids[0], ids[1]);
       *reinterpret_cast<longlong2*>(a.slot_map + i0) = make_longlong2(slot[0], slot[1]);
-      *reinterpret_cast<longlong2*>(a.slot_map + i0 + 2) = make_longlong2(slot[2], slot[3]);
     } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i0 + e < end) {
-          a.positions[i0 + e] = pos[e];
-          a.seq_ids[i0 + e] = ids[e];
-          a.slot_map[i0 + e] = slot[e];
-        }
+      a.positions[i0] = pos[0];
+      a.seq_ids[i0] = ids[0];
+      a.slot_map[i0] = slot[0];
     }
   }
 }
 
-// One CTA: the scans, cu_new, the pages before each sequence (workspace) and the free count left;
-// with EXPAND it then writes the tokens too.  Workspace: [0] free ids at the start, [1] tokens of the plan,
-// [4 + b] new pages of the sequences before b.
-template <bool EXPAND>
+// One launch: every CTA scans all requests (eight consecutive ones per thread) into shared memory and writes its chunk of
+// the tokens; the first also writes cu_new, and the last one to have read the free count writes what is left of it
+// (which may be the same word).  Workspace: [0] counts the CTAs that have read it, back to 0 at the end.
+__global__ void __launch_bounds__(kPlanThreads) plan_once_kernel(Geom g, PlanArgs a, int chunk) {
+  __shared__ int32_t cu[kPlanOnce + 1], before[kPlanOnce], len[kPlanOnce];
+  __shared__ longlong2 warp_tot[kPlanThreads / 32];
+  __shared__ longlong2 s_tot;
+  __shared__ int s_free, s_last, s_range[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    s_free = max(0, min(*reinterpret_cast<const volatile int32_t*>(a.free_count), a.free_cap));
+    s_tot = make_longlong2(0, 0);
+    __threadfence();
+    s_last = atomicInc(reinterpret_cast<unsigned*>(a.ws), gridDim.x - 1) == gridDim.x - 1;
+  }
+  const int items = (g.B + kPlanThreads - 1) / kPlanThreads, b0 = tid * items;
+  longlong2 mine[kPlanItems], sum = make_longlong2(0, 0);
+#pragma unroll
+  for (int i = 0; i < kPlanItems; ++i) {
+    mine[i] = make_longlong2(0, 0);
+    const int b = b0 + i;
+    if (i < items && b < g.B) {
+      bool bad;
+      mine[i] = request(g, a, b, bad);
+      len[b] = g.seq_len[b];
+      if (bad && blockIdx.x == 0) set_status(g.status, KVQ_DEV_OVERFLOW);
+    }
+    sum = add2ll(sum, mine[i]);
+  }
+  longlong2 upto = warp_scan(sum, lane);
+  if (lane == 31) warp_tot[warp] = upto;
+  __syncthreads();
+  const int64_t free_n = s_free;
+  for (int w = 0; w < warp; ++w) upto = add2ll(upto, warp_tot[w]);
+  longlong2 at = make_longlong2(upto.x - sum.x, upto.y - sum.y);  // before this thread's requests
+  int n_mine = 0;  // served ones of them: the sums only grow, so the first
+  longlong2 end = at;
+#pragma unroll
+  for (int i = 0; i < kPlanItems; ++i) {
+    const int b = b0 + i;
+    if (i < items && b < g.B) {
+      const longlong2 next = add2ll(at, mine[i]);
+      const bool served = next.x <= a.max_tokens && next.y <= free_n;
+      if (served) {
+        cu[b + 1] = (int32_t)next.x;
+        before[b] = (int32_t)at.y;
+        end = next;
+        ++n_mine;
+      } else if (mine[i].x > 0 && blockIdx.x == 0) {
+        set_status(g.status, next.y > free_n ? KVQ_DEV_NO_PAGES : KVQ_DEV_OVERFLOW);
+      }
+      at = next;
+    }
+  }
+  // the served requests are the first ones, so the last thread that has any knows the totals
+  const int with_any = __syncthreads_count(n_mine > 0);
+  if (tid == with_any - 1) s_tot = end;
+  __syncthreads();
+  const longlong2 tot = s_tot;
+#pragma unroll
+  for (int i = 0; i < kPlanItems; ++i) {
+    const int b = b0 + i;
+    if (i < items && b < g.B && i >= n_mine) {
+      cu[b + 1] = (int32_t)tot.x;
+      before[b] = (int32_t)tot.y;
+    }
+  }
+  if (tid == 0) cu[0] = 0;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= g.B; b += kPlanThreads) a.cu[b] = cu[b];
+  if (tid == 0 && s_last) *a.free_left = (int32_t)(free_n - tot.y);
+  const int64_t begin = (int64_t)blockIdx.x * chunk;
+  if (begin < tot.x) {
+    const int last = (int)min(tot.x, (long long)(begin + chunk));
+    if (tid < 2) s_range[tid] = seq_of(cu, tid ? last - 1 : (int)begin, 0, g.B - 1);  // the chunk's sequences
+    __syncthreads();
+    expand(g, a, cu, before, len, (int)begin, last, s_range[0], s_range[1], (int)free_n);
+  }
+}
+
+// More sequences, two launches: one CTA makes the scans, cu_new, the pages before each sequence (workspace) and the free
+// count left; then the tokens.  Workspace: [1] free ids at the start, [2] tokens of the plan, [4 + b] new pages before b.
 __global__ void __launch_bounds__(kPlanScan) plan_scan_kernel(Geom g, PlanArgs a) {
   __shared__ longlong2 warp_tot[32];
   __shared__ longlong2 s_tot;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  if constexpr (!EXPAND) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t free_n = max(0, min(*a.free_count, a.free_cap));
   longlong2 carry = make_longlong2(0, 0);  // sums of the rounds before
   int n_served = 0;
@@ -139,53 +215,52 @@ __global__ void __launch_bounds__(kPlanScan) plan_scan_kernel(Geom g, PlanArgs a
   }
   if (tid == 0) {
     a.cu[0] = 0;
-    a.ws[0] = (int32_t)free_n;
-    a.ws[1] = (int32_t)tot.x;
+    a.ws[1] = (int32_t)free_n;
+    a.ws[2] = (int32_t)tot.x;
     *a.free_left = (int32_t)(free_n - tot.y);
-  }
-  if constexpr (EXPAND) {
-    __syncthreads();
-    expand(g, a, 0, (int)tot.x, 0, g.B - 1, (int)free_n, tid, blockDim.x);
   }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_expand_kernel(Geom g, PlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads) plan_expand_kernel(Geom g, PlanArgs a, int chunk) {
   __shared__ int s_range[2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int total = a.ws[1], begin = blockIdx.x * kPlanChunk;
+  const int total = a.ws[2];
+  const int64_t begin = (int64_t)blockIdx.x * chunk;
   if (begin >= total) return;
-  const int end = min(total, begin + kPlanChunk);
-  if (threadIdx.x < 2) {  // the sequences of the chunk's first and last token
-    const int i = threadIdx.x ? end - 1 : begin;
-    s_range[threadIdx.x] = seq_of(a.cu, i, 0, g.B - 1);
-  }
+  const int end = (int)min((int64_t)total, begin + chunk);
+  if (threadIdx.x < 2)  // the sequences of the chunk's first and last token
+    s_range[threadIdx.x] = seq_of(a.cu, threadIdx.x ? end - 1 : (int)begin, 0, g.B - 1);
   __syncthreads();
-  expand(g, a, begin, end, s_range[0], s_range[1], a.ws[0], threadIdx.x, kPlanThreads);
+  expand(g, a, a.cu, a.ws + 4, g.seq_len, (int)begin, end, s_range[0], s_range[1], a.ws[1]);
 }
 
 }  // namespace
 
 size_t plan_workspace(const Geom& g) { return ((size_t)g.B + 4) * sizeof(int32_t); }
 
-// Few tokens (a decode step): one launch.  Else the scan, and an expansion whose launch overlaps it.
 cudaError_t launch_plan(const Geom& g, const PlanArgs& a, cudaStream_t st) {
-  if (a.max_tokens <= kPlanOneCta) {
-    plan_scan_kernel<true><<<1, kPlanScan, 0, st>>>(g, a);
+  // Measured on one B200, one launch against two: 256 sequences of one token 5.0 / 7.2 us, 2000 of 100 8.7 / 10.5 us,
+  // 32 of 16384 6.2 / 6.6 us, 256 of 4096 10.7 / 8.1 us, 256 of 16384 22 / 17 us.
+  const bool once = g.B <= kPlanOnce && a.max_tokens <= kOnceTokens;
+  const int chunk = once ? 1024 : 2048;  // tokens of a CTA
+  const unsigned grid = (unsigned)std::max<int64_t>(1, (a.max_tokens + chunk - 1) / chunk);
+  if (once) {
+    plan_once_kernel<<<grid, kPlanThreads, 0, st>>>(g, a, chunk);
     return cudaGetLastError();
   }
-  plan_scan_kernel<false><<<1, kPlanScan, 0, st>>>(g, a);
+  plan_scan_kernel<<<1, std::min(kPlanScan, (g.B + 127) / 128 * 128), 0, st>>>(g, a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at{};
+  cudaLaunchAttribute at{};  // the expansion's launch overlaps the scan
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((a.max_tokens + kPlanChunk - 1) / kPlanChunk));
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, plan_expand_kernel, g, a);
+  return cudaLaunchKernelEx(&cfg, plan_expand_kernel, g, a, chunk);
 }
 
 }  // namespace kvq

@@ -353,7 +353,9 @@ KVQ_API kvq_status kvq_norm_rope(const kvq_rows* q, const kvq_rows* k, const kvq
  * A request with a negative length or past the page table flags KVQ_DEV_OVERFLOW and gets nothing.
  * When the tokens would pass max_tokens (KVQ_DEV_OVERFLOW) or the pages the stack
  * (KVQ_DEV_NO_PAGES), that sequence and all after it get nothing.
- * slot_map, positions and seq_ids are 16-byte aligned.  Workspace: kvq_plan_workspace_bytes().
+ * slot_map, positions and seq_ids are 16-byte aligned.
+ * Workspace: kvq_plan_workspace_bytes(), 4-byte aligned, ZERO-FILLED before its first use (its counter is left at
+ * zero again).  Two calls in flight at once on one workspace race.
  */
 KVQ_API size_t kvq_plan_workspace_bytes(const kvq_cache* cache);
 KVQ_API kvq_status kvq_plan_pages(const kvq_cache* cache, const int32_t* new_len, const int32_t* free_pages,
