@@ -269,6 +269,9 @@ kvq_status kvq_norm_rope(const kvq_rows* q, const kvq_rows* k, const kvq_rows* v
     if (r->in_tok_stride % 8 || r->in_head_stride % 8 || r->out_tok_stride % 8 || r->out_head_stride % 8 ||
         r->in_tok_stride < 0 || r->in_head_stride < 0 || r->out_tok_stride < 0 || r->out_head_stride < 0)
       return fail(KVQ_ERR_INVALID_ARG, "strides must be multiples of 8 elements, not negative");
+    if ((r->heads > 1 && r->out_head_stride < 128) || (num_tokens > 1 && r->out_tok_stride < 128))
+      return fail(KVQ_ERR_INVALID_ARG, "output rows overlap (strides %lld, %lld)", (long long)r->out_tok_stride,
+                  (long long)r->out_head_stride);
     if (i == 2 && r->weight) return fail(KVQ_ERR_INVALID_ARG, "values take no weight");
     a.rows[i] = {r->in, r->out, r->weight, r->heads, r->in_tok_stride, r->in_head_stride, r->out_tok_stride,
                  r->out_head_stride};

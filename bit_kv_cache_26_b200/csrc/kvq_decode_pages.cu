@@ -24,9 +24,9 @@
 // eight heads, and a second product adds the lo parts.
 //
 // The newest incomplete page takes its keys from the K tail, exact 16-bit operands of the same
-// products.  W is summed in fixed point by integer atomics (2^-19 of the largest weight a warp has
-// met; at most 2048 tokens per warp, so no overflow): whole numbers, so the order does not matter
-// and results do not depend on timing.
+// products.  W is summed in fixed point by integer atomics (units of 2^-19 of the largest weight a
+// head has met in a warp; at most 2048 tokens per warp, so no overflow): whole numbers, so the order
+// does not matter and results do not depend on timing.
 #include <algorithm>
 #include <atomic>
 
@@ -84,6 +84,10 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// 2^e, to the range of normal numbers; the smallest power of two above a number >= 0 (or one below all normal ones).
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + max(-126, min(127, e))) << 23); }
+__device__ __forceinline__ int exponent_above(float x) { return (int)(__float_as_uint(x) >> 23 & 0xff) - 126; }
 
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   uint32_t h;
@@ -352,12 +356,14 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 
     // ---- per-thread state
     float accv[NT][8][4], zacc[NT][HPT][4], mrun[NT][HPT], lrun[NT][HPT], scl[NT][HPT];
+    int vexp[NT][HPT];  // accv is in units of 2^vexp, the pattern weights of 2^(vexp - kWBits); no weight p r is above 2^vexp
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int x = 0; x < HPT; ++x) {
         mrun[j][x] = -INFINITY;
         lrun[j][x] = 0.f;
+        vexp[j][x] = g.tx ? -100 : 0;  // (without row factors a weight is at most 1)
         scl[j][x] = a.scale_log2 * qinv[TH * j + HPT * tig + x];
 #pragma unroll
         for (int u = 0; u < 4; ++u) zacc[j][x][u] = 0.f;
@@ -368,7 +374,6 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         for (int u = 0; u < 4; ++u) accv[j][mt][u] = 0.f;
     }
 
-    int vexp = g.tx ? -100 : 0;  // pattern weights are in units of 2^(vexp - kWBits): vexp grows with the row factors
     int stuck_at = -1;
     for (int i = 0; i < my_n; ++i) {
       const int st = i % kStages;
@@ -524,22 +529,11 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         int vi[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) vi[u] = min((int)((vidx4 >> (8 * u)) & 0xff), P);
-        float wscale = (float)(1 << kWBits), wshrink = 1.0f;
-        if (g.tx) {  // the row factors' running power of two
-          const float most = fmaxf(fmaxf(vrow[0], vrow[1]), fmaxf(vrow[2], vrow[3]));
-          const int e = max(-100, min(100, (int)(__reduce_max_sync(kFull, __float_as_uint(most)) >> 23 & 0xff) - 126));
-          if (e > vexp) {
-            wshrink = __uint_as_float((uint32_t)max(0, 127 + vexp - e) << 23);
-            vexp = e;
-          }
-          wscale = __uint_as_float((uint32_t)(127 + kWBits - vexp) << 23);
-        }
-
         // ---- online softmax (base 2), per head over the 32 tokens
         float p0[4];  // narrow: p of this lane's four V columns' tokens
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          float mnew[HPT], alpha[HPT];
+          float pv[HPT][4], p[HPT][4], alpha[HPT], wfactor[HPT];
           bool same = true;
 #pragma unroll
           for (int x = 0; x < HPT; ++x) {
@@ -547,11 +541,27 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
             pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 4));
             pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 8));
             pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, 16));
-            const float m = fmaxf(mrun[j][x], pm);
-            mnew[x] = m == -INFINITY ? 0.f : m;
-            alpha[x] = ex2(mrun[j][x] - mnew[x]);
+            const float m = fmaxf(mrun[j][x], pm), base = m == -INFINITY ? 0.f : m;
+            alpha[x] = ex2(mrun[j][x] - base);
             mrun[j][x] = m;
-            same = same && alpha[x] * wshrink == 1.0f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              p[x][u] = TH * j + HPT * tig + x < Gq ? ex2(sc[j][x][u] - base) : 0.f;
+              pv[x][u] = p[x][u] * vrow[u];
+            }
+            wfactor[x] = alpha[x];
+            if (g.tx) {
+              // p r has no bound of its own: the unit follows the largest so far, as far as that still counts
+              float most = fmaxf(fmaxf(pv[x][0], pv[x][1]), fmaxf(pv[x][2], pv[x][3]));
+              most = fmaxf(most, __shfl_xor_sync(kFull, most, 4));
+              most = fmaxf(most, __shfl_xor_sync(kFull, most, 8));
+              most = fmaxf(most, __shfl_xor_sync(kFull, most, 16));
+              const int now = exponent_above(most), was = vexp[j][x] + (alpha[x] == 1.0f ? 0 : exponent_above(alpha[x]));
+              const int e = max(-100, min(100, max(now, was)));
+              wfactor[x] *= exp2i(vexp[j][x] - e);
+              vexp[j][x] = e;
+            }
+            same = same && alpha[x] == 1.0f && wfactor[x] == 1.0f;
           }
           if (!__all_sync(kFull, same)) {
 #pragma unroll
@@ -564,42 +574,43 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
               for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                  if (!WIDE || (u & 1) == x) accv[j][mt][u] *= alpha[x];
+                  if (!WIDE || (u & 1) == x) accv[j][mt][u] *= wfactor[x];
               for (int jj = gq; jj < Pe; jj += 8)
-                Ww[hh * WR + jj] = __float2int_rn((float)Ww[hh * WR + jj] * (alpha[x] * wshrink));
+                Ww[hh * WR + jj] = __float2int_rn((float)Ww[hh * WR + jj] * wfactor[x]);
             }
             __syncwarp();
           }
 #pragma unroll
           for (int x = 0; x < HPT; ++x) {
             const int hh = TH * j + HPT * tig + x;
-            const bool real = hh < Gq;
-            float pv[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const float p = real ? ex2(sc[j][x][u] - mnew[x]) : 0.f;
-              lrun[j][x] += p;
-              pv[u] = p * vrow[u];
-              zacc[j][x][0] = fmaf(pv[u], vz[u].x, zacc[j][x][0]);
-              zacc[j][x][1] = fmaf(pv[u], vz[u].y, zacc[j][x][1]);
-              zacc[j][x][2] = fmaf(pv[u], vz[u].z, zacc[j][x][2]);
-              zacc[j][x][3] = fmaf(pv[u], vz[u].w, zacc[j][x][3]);
+              lrun[j][x] += p[x][u];
+              zacc[j][x][0] = fmaf(pv[x][u], vz[u].x, zacc[j][x][0]);
+              zacc[j][x][1] = fmaf(pv[x][u], vz[u].y, zacc[j][x][1]);
+              zacc[j][x][2] = fmaf(pv[x][u], vz[u].z, zacc[j][x][2]);
+              zacc[j][x][3] = fmaf(pv[x][u], vz[u].w, zacc[j][x][3]);
             }
-            if (real) {
+            if (g.tx) {
+              const float unit = exp2i(-vexp[j][x]);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) pv[x][u] *= unit;
+            }
+            if (hh < Gq) {
 #pragma unroll
               for (int u = 0; u < 4; ++u)  // rounded to whole units by the addition of 1.5 * 2^23
-                atomicAdd(&Ww[hh * WR + vi[u]], __float_as_int(fmaf(pv[u], wscale, 12582912.0f)) - 0x4B400000);
+                atomicAdd(&Ww[hh * WR + vi[u]], __float_as_int(fmaf(pv[x][u], (float)(1 << kWBits), 12582912.0f)) - 0x4B400000);
             }
             // p to the lanes of the V columns, scaled; tokens 8..15 of each 16 are columns with a factor of their own
             constexpr float f0 = kVFac, f8 = kVFac / Code<BITS>::kCol;
             if constexpr (WIDE) {
-              *reinterpret_cast<float4*>(pex + hh * kPexRow + gq * 4) = make_float4(pv[0] * f0, pv[1] * f8, pv[2] * f0, pv[3] * f8);
+              *reinterpret_cast<float4*>(pex + hh * kPexRow + gq * 4) = make_float4(pv[x][0] * f0, pv[x][1] * f8, pv[x][2] * f0, pv[x][3] * f8);
             } else {
               // Lane (head, part) wants tokens 2 tig and 2 tig + 1 (+ 8) of the page's half `part`: u = 2 part, 2 part + 1.
               // Even token rows offer the halves in one order, odd rows in the other, so that both exchanges serve both
               // parts; part 1 gets 2 tig + 1 first (and reads its scales in that order: no bank conflict with part 0).
-              const float y0 = (part ? pv[2] : pv[0]) * f0, y1 = (part ? pv[3] : pv[1]) * f8;
-              const float z0 = (part ? pv[0] : pv[2]) * f0, z1 = (part ? pv[1] : pv[3]) * f8;
+              const float y0 = (part ? pv[x][2] : pv[x][0]) * f0, y1 = (part ? pv[x][3] : pv[x][1]) * f8;
+              const float z0 = (part ? pv[x][0] : pv[x][2]) * f0, z1 = (part ? pv[x][1] : pv[x][3]) * f8;
               const int src = 8 * tig + (gq >> 1) + 4 * part;  // row 2 tig + part
               p0[0] = __shfl_sync(kFull, y0, src);
               p0[1] = __shfl_sync(kFull, z0, src ^ 4);
@@ -730,7 +741,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 #pragma unroll
       for (int x = 0; x < HPT; ++x) {
         const int hh = TH * j + HPT * tig + x;
-        constexpr float f0 = 16777216.0f / kVFac, f8 = 16777216.0f / kVFac / Code<BITS>::kRow;
+        const float f0 = 16777216.0f / kVFac * exp2i(vexp[j][x]), f8 = f0 / Code<BITS>::kRow;
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
           mo[(warp * NH + hh) * kD + 16 * mt + gq] = (WIDE ? accv[j][mt][x] : accv[j][mt][0] + accv[j][mt][1]) * f0;
@@ -739,7 +750,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         if (gq == 0) {
           mm[warp * NH + hh] = mrun[j][x];
           ml[warp * NH + hh] = lrun[j][x];
-          munit[warp * NH + hh] = __uint_as_float((uint32_t)(127 - kWBits + vexp) << 23);
+          munit[warp * NH + hh] = exp2i(vexp[j][x] - kWBits);
 #pragma unroll
           for (int u = 0; u < 4; ++u) mz[(warp * NH + hh) * 4 + u] = zacc[j][x][u];
         }

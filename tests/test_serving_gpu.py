@@ -172,6 +172,7 @@ def check_plan(kvq, L, n, maxp, free_n=None, most=None, seed=0, want_bits=None):
 @pytest.mark.parametrize("L,n,maxp", [
     ([0], [1], 1), ([31], [1], 1), ([32], [1], 2), ([5, 0, 64, 31], [0, 0, 0, 0], 3), ([5, 0, 64, 31, 32], [1, 1, 1, 1, 1], 3),
     ([0, 100, 0, 7], [65, 0, 31, 33], 4), ([17] * 300, [1] * 300, 2), ([0] * 3, [5000, 0, 4001], 160), ([40, 3], [4096, 8191], 400),
+    ([100, 0], [530000, 7], 16600),
 ])
 def test_plan(kvq, L, n, maxp):
     check_plan(kvq, L, n, maxp)
@@ -293,7 +294,7 @@ def check_select(kvq, cache, q, bounds, budget, sink, recent, ws=None):
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("H,Gq,L,budget,sink,recent", [
     (1, 1, [1], 1, 0, 1), (1, 4, [33, 0, 32], 1, 0, 1), (2, 7, [1000, 0, 31, 96], 3, 1, 2), (2, 16, [2048, 2047], 8, 1, 1),
-    (3, 5, [4099, 17, 640], 20, 0, 1), (1, 8, [20000], 64, 3, 5), (4, 4, [9000] * 3, 63, 1, 2), (1, 2, [300000], 200, 1, 4),
+    (3, 5, [4099, 17, 640], 20, 0, 1), (1, 3, [70000 * 32 - 5], 33, 2, 3), (1, 8, [20000], 64, 3, 5), (4, 4, [9000] * 3, 63, 1, 2), (1, 2, [300000], 200, 1, 4),
 ])
 def test_select_pages(kvq, dtype, H, Gq, L, budget, sink, recent):
     dt, g, B = DT[dtype], gen(budget), len(L)
@@ -393,7 +394,8 @@ def attend_reference(kvq, cache, q, lists, counts, scale):
 
     A logit is a sum of q_d s_d code, q_d z_d and q_d M_d, each below |q_d| 4 R_d (R the largest |k_d|), carried with 21 or
     more bits: off by at most delta = 2^-20 12 scale sum_d |q_d| R_d.  A softmax weight is then off by 2 delta of itself,
-    and so is the output, of max |v|; p s code, p z and W M add 2^-20 12 max |v|."""
+    which moves the output by 2 delta S, S = sum_t p_t max |v_t|; p s code, p z and W M, carried alike, by 2^-20 12 S; and
+    each of the n tokens' weights in W is rounded to 2^-20 of the largest, 4 max_t p_t max |v_t| 2^-20 in the output."""
     B, H = cache.B, cache.H
     Gq = q.shape[1] // H
     out = torch.zeros(B, H * Gq, D, dtype=torch.float64, device="cuda")
@@ -412,7 +414,8 @@ def attend_reference(kvq, cache, q, lists, counts, scale):
             p = torch.softmax(qs @ k[t, h].T * scale, -1)
             out[b, h * Gq:(h + 1) * Gq] = p @ v[t, h]
             delta = 2.0 ** -20 * 12 * scale * (qs.abs() @ k[:, h].abs().amax(0))
-            err[b, h * Gq:(h + 1) * Gq, 0] = (2 * delta + 2.0 ** -20 * 12) * v[:, h].abs().max()
+            each = p * v[t, h].abs().amax(-1)
+            err[b, h * Gq:(h + 1) * Gq, 0] = (2 * delta + 2.0 ** -20 * 12) * each.sum(-1) + len(t) * 2.0 ** -20 * 4 * each.amax(-1)
     return out, err
 
 
@@ -527,6 +530,23 @@ def test_attention_of_extreme_rows(kvq):
     within(attend(cache, q, lists, n), *attend_reference(kvq, cache, q, lists, n, D ** -0.5))
 
 
+def test_attention_when_the_largest_row_factors_do_not_count(kvq):
+    # under the pre-transform, a page whose values are 2^14 times the others' but whose keys score far below
+    cache = filled(kvq, 1, 1, 0, 4, 8, torch.float16, tx=1, lengths=[320])
+    cb = 32 * D * 4 // 8
+    for page, factor in ((3, 2.0 ** 14), (7, 2.0 ** -6)):
+        f = cache.subblock(0, page, 0).view(torch.float32)
+        f[(2 * cb + 2112) // 4:(2 * cb + 2240) // 4] = 0.0           # its keys are zero vectors
+        f[(2 * cb + 2240) // 4:] *= factor
+    q = (6 * randn(gen(3), 1, 4, D)).to(torch.float16)
+    for order in ([3, 0, 1, 2, 4, 5, 6, 7, 8, 9], [9, 8, 7, 3, 2, 1, 0]):
+        lists = torch.tensor(order, dtype=torch.int32, device="cuda").view(1, 1, -1).contiguous()
+        n = torch.full((1, 1), len(order), dtype=torch.int32, device="cuda")
+        want, err = attend_reference(kvq, cache, q, lists, n, D ** -0.5)
+        assert float(want.abs().max()) < 100                         # page 3 has no weight
+        within(attend(cache, q, lists, n), want, err)
+
+
 # ---- streams, graphs, devices --------------------------------------------------------------------
 
 def test_a_captured_step_replays_on_new_inputs(kvq):
@@ -591,6 +611,59 @@ def test_a_captured_step_replays_on_new_inputs(kvq):
             within(eager.out, *attend_reference(kvq, eager.c, eager.q, eager.lists, eager.n, D ** -0.5))
     assert torch.equal(eager.bounds, replay.bounds)
     assert eager.c.read_status() == 0 and replay.c.read_status() == 0
+
+
+@pytest.mark.parametrize("B", [3, 2100])
+def test_a_captured_plan_pops_the_stack_on_every_replay(kvq, B):
+    # both forms of the call (one launch, two): three steps of a token each, by replays of one graph
+    L, n, maxp = [31] * B, [1] * B, 3
+    cache, t, table, free, free_n, most = make_plan(kvq, L, n, maxp)
+    ws = cache.plan_workspace()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        cache.plan(t["new"], t["free"], t["count"], t["cu"], t["slots"][:most], t["pos"][:most], t["ids"][:most], ws)
+        cache.seq_len.add_(1)
+    torch.cuda.current_stream().wait_stream(s)
+    left = free_n
+    for step in range(35):
+        graph.replay()
+        table, cu, slots, pos, ids, left, bits = plan_reference([31 + step] * B, n, table, free, left, most)
+        if step in (0, 1, 33, 34):
+            assert np.array_equal(cache.page_table.cpu().numpy(), table) and int(t["count"]) == left
+            assert t["slots"][:most].tolist() == slots and t["pos"][:most].tolist() == pos and t["ids"][:most].tolist() == ids
+    assert cache.read_status() == 0
+
+
+FAILURE = """
+    import sys
+    sys.path.insert(0, {root!r})
+    sys.path.insert(0, {tests!r})
+    import torch
+    import bit_kv_cache_26_b200 as kvq
+    from test_serving_gpu import attend, filled, gen, random_lists, randn
+    cache = filled(kvq, 2, 2, 0, 4, 8, torch.bfloat16, lengths=[300, 40])
+    lists, n = random_lists(cache, 10, 0)
+    attend(cache, randn(gen(0), 2, 8, 128).to(torch.bfloat16), lists, n)
+    bits = cache.read_status(clear=True)
+    assert bits & kvq.KVQ_DEV_TIMEOUT, hex(bits)
+    assert torch.arange(1 << 20, device="cuda").sum().item() == (1 << 19) * ((1 << 20) - 1)
+    print("timeout flagged")
+"""
+
+
+def test_expired_page_waits_are_flagged():
+    # every page wait gives up at once: the status says so, the copies in flight are waited for, the context stays usable
+    import os
+    import subprocess
+    import sys
+    import textwrap
+
+    from conftest import ROOT
+    code = textwrap.dedent(FAILURE).format(root=ROOT, tests=os.path.join(ROOT, "tests"))
+    r = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, KVQ_TEST_WAIT_LIMIT="0"), capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "timeout flagged" in r.stdout, r.stdout + r.stderr
 
 
 def test_calls_on_a_stream_of_their_own(kvq):

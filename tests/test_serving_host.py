@@ -48,7 +48,7 @@ def rope(q=None, k=None, v=None, dtype=1, tokens=4, pos=256, inv=256, rot=128, e
     (dict(q=rows(out=260)), INVALID), (dict(q=rows(weight=8)), INVALID), (dict(q=rows(heads=-1)), INVALID),
     (dict(q=rows(in_tok_stride=132)), INVALID), (dict(q=rows(out_head_stride=4)), INVALID),
     (dict(q=rows(in_head_stride=-128)), INVALID), (dict(q=rows(reserved=1)), INVALID), (dict(q=rows(heads=65536)), CAPACITY),
-    (dict(v=rows(weight=256)), INVALID),
+    (dict(v=rows(weight=256)), INVALID), (dict(q=rows(out_head_stride=0)), INVALID), (dict(q=rows(out_tok_stride=64)), INVALID),
 ])
 def test_norm_rope_refuses(kw, status):
     assert rope(**{"q": rows(), **kw}) == status
