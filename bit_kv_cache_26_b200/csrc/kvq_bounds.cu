@@ -15,6 +15,7 @@
 //   term_d = fl(fl(W+_d hi_d) + fl(W-_d lo_d)); 8 neighbouring channels halved (4, 2, 1), then
 //   the 16 sums halved (8, 4, 2, 1).  Equal scores: the lower page.  NaN ranks above all.
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
@@ -99,10 +100,13 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) page_bounds_kernel(Geom g, 
 
 // ---- selection -------------------------------------------------------------------------------
 
-constexpr int kSelThreads = 256;
+constexpr int kSelThreads = 128;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelAhead = 4;           // pages in flight per 16 lanes
-constexpr int kSelKeys = 8192;         // keys that fit in shared memory
+constexpr int kSelAhead = 4;           // pages of a round per 16 lanes
+constexpr int kSelRounds = 2;          // rounds in flight
+constexpr int kSelRing = kSelRounds * kSelAhead * 2 * kSelThreads * 16;  // bytes: 16 of lo and of hi per lane and page
+constexpr int kLocalKeys = 1024;       // keys that stay in shared memory when one CTA scores all pages
+constexpr int kSelKeys = kSelRing / 4; // keys that fit in the ring's place when the scores are all there
 
 // fp32 -> unsigned with the same order; -0 is +0, NaN above all.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -123,13 +127,15 @@ __device__ __forceinline__ unsigned long long widen(uint32_t u) {
   return pk(f.x, f.y);
 }
 
-// Scores of pages [p0, p1) of (b, h) as ordered keys, keys[p - lo_page]: 16 lanes per page, 8 channels per lane, four
-// pages in flight; their four sums over the lanes share the exchanges (after a step that halves the lanes a value
-// is spread over, each half of the lanes goes on with half of the values).
+// Scores of pages [p0, p1) of (b, h) as ordered keys, keys[p - lo_page]: 16 lanes per page, 8 channels per lane.  Every lane
+// copies its own 32 bytes of a page into its own places of the ring (so it waits for its own copies only) and has two
+// rounds of four pages in flight; the four sums over the lanes share the exchanges (after a step that halves the lanes a
+// value is spread over, each half of the lanes goes on with half of the values).
 template <bool BF16>
 __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int Gq, const uint16_t* __restrict__ bounds, int b,
-                            int h, int p0, int p1, int lo_page, uint32_t* keys, float* W) {
-  static_assert(kSelAhead == 4, "the exchange below is written for four pages");
+                            int h, int p0, int p1, int lo_page, uint32_t* keys, float* W, uint8_t* ring) {
+  static_assert(kSelAhead == 4 && kSelRounds == 2, "the exchanges and waits below are written for these");
+  constexpr int kStep = 2 * kSelAhead * kSelWarps;  // pages of a round of the block
   const int lane = threadIdx.x & 31, c = lane & 15, sub = lane >> 4;
   const int32_t* table = g.page_table + (int64_t)b * g.maxp;
   const int first = p0 + 2 * kSelAhead * (threadIdx.x >> 5) + kSelAhead * sub;
@@ -144,20 +150,48 @@ __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int G
       }
     }
   };
+  const uint16_t* mine = bounds + (int64_t)h * 2 * kD + 8 * c;
+  const int64_t page_stride = (int64_t)g.H * 2 * kD;
+  uint8_t* place = ring + threadIdx.x * 16;  // + (round, page, lo / hi) * the block's threads * 16
+  unsigned gone[kSelRounds] = {0u, 0u};      // pages of the round that have no valid id
+  auto issue = [&](int round) {
+    unsigned none = 0;
+#pragma unroll
+    for (int i = 0; i < kSelAhead; ++i) {
+      if (phys[i] >= 0) {
+        const uint16_t* src = mine + phys[i] * page_stride;
+        const uint32_t dst = smem_u32(place + (round * kSelAhead + i) * 2 * kSelThreads * 16);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + kSelThreads * 16), "l"(src + kD) : "memory");
+      } else {
+        none |= 1u << i;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    gone[round] = none;
+  };
   load_ids(first);
-  {  // W+ (threads 0..127) and W- (128..255)
-    const int d = threadIdx.x & (kD - 1);
-    const bool neg = threadIdx.x >= kD;
+  issue(0);
+  load_ids(first + kStep);
+  issue(1);
+  load_ids(first + 2 * kStep);
+  static_assert(kSelThreads == kD, "a thread per channel of W+ and W-");
+  {
     float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < Gq ? load_elem(q + ((int64_t)b * g.H * Gq + (int64_t)h * Gq + i) * kD + d, g.dtype) : 0.f;
+    for (int i = 0; i < 16; ++i)
+      v[i] = i < Gq ? load_elem(q + ((int64_t)b * g.H * Gq + (int64_t)h * Gq + i) * kD + threadIdx.x, g.dtype) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = v[i] != v[i] ? v[i] : neg ? fminf(v[i], 0.f) : fmaxf(v[i], 0.f);
+    for (int neg = 0; neg < 2; ++neg) {
+      float w[16];
 #pragma unroll
-    for (int o = 8; o; o >>= 1)
+      for (int i = 0; i < 16; ++i) w[i] = v[i] != v[i] ? v[i] : neg ? fminf(v[i], 0.f) : fmaxf(v[i], 0.f);
 #pragma unroll
-      for (int i = 0; i < o; ++i) v[i] = __fadd_rn(v[i], v[i + o]);
-    W[threadIdx.x] = v[0];
+      for (int o = 8; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) w[i] = __fadd_rn(w[i], w[i + o]);
+      W[neg * kD + threadIdx.x] = w[0];
+    }
   }
   __syncthreads();
   unsigned long long up[4], dn[4];
@@ -166,27 +200,14 @@ __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int G
     up[e] = pk(W[8 * c + 2 * e], W[8 * c + 2 * e + 1]);
     dn[e] = pk(W[kD + 8 * c + 2 * e], W[kD + 8 * c + 2 * e + 1]);
   }
-  const uint16_t* mine = bounds + (int64_t)h * 2 * kD + 8 * c;
-  const int64_t page_stride = (int64_t)g.H * 2 * kD;
-  for (int p = first; p - kSelAhead * sub < p1; p += 2 * kSelAhead * kSelWarps) {
-    uint4 lo[kSelAhead], hi[kSelAhead];
-    bool none[kSelAhead];
-#pragma unroll
-    for (int i = 0; i < kSelAhead; ++i) {
-      lo[i] = hi[i] = make_uint4(0u, 0u, 0u, 0u);
-      none[i] = phys[i] < 0;
-      if (!none[i]) {
-        const uint16_t* src = mine + phys[i] * page_stride;
-        lo[i] = __ldg(reinterpret_cast<const uint4*>(src));
-        hi[i] = __ldg(reinterpret_cast<const uint4*>(src + kD));
-      }
-    }
-    load_ids(p + 2 * kSelAhead * kSelWarps);
+  auto round = [&](int p, int r) {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the newest round
     float x[kSelAhead];
 #pragma unroll
     for (int i = 0; i < kSelAhead; ++i) {
-      const uint32_t* l = &lo[i].x;
-      const uint32_t* u = &hi[i].x;
+      const uint8_t* from = place + (r * kSelAhead + i) * 2 * kSelThreads * 16;
+      const uint4 lo = *reinterpret_cast<const uint4*>(from), hi = *reinterpret_cast<const uint4*>(from + kSelThreads * 16);
+      const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, u[4] = {hi.x, hi.y, hi.z, hi.w};
       unsigned long long t[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) t[e] = addp(mul2(up[e], widen<BF16>(u[e])), mul2(dn[e], widen<BF16>(l[e])));
@@ -194,6 +215,9 @@ __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int G
       upk(addp(addp(t[0], t[2]), addp(t[1], t[3])), s0, s1);
       x[i] = __fadd_rn(s0, s1);
     }
+    const unsigned none = gone[r];
+    issue(r);  // the round after the next, into the places just read
+    load_ids(p + 3 * kStep);
     // lanes with bit 3: pages 2 and 3; of those, lanes with bit 2: the odd one
     const bool b3 = c & 8, b2 = c & 4;
     const float y0 = __fadd_rn(b3 ? x[2] : x[0], __shfl_xor_sync(kFull, b3 ? x[0] : x[2], 8));
@@ -202,28 +226,30 @@ __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int G
     z = __fadd_rn(z, __shfl_xor_sync(kFull, z, 2));
     z = __fadd_rn(z, __shfl_xor_sync(kFull, z, 1));
     const int i = (b3 ? 2 : 0) + (b2 ? 1 : 0);
-    if ((c & 3) == 0 && p + i < p1) {
-      const bool gone = b3 ? (b2 ? none[3] : none[2]) : (b2 ? none[1] : none[0]);
-      keys[p + i - lo_page] = gone ? 0u : order_key(z);
-    }
+    if ((c & 3) == 0 && p + i < p1) keys[p + i - lo_page] = none >> i & 1 ? 0u : order_key(z);
+  };
+  for (int p = first; p - kSelAhead * sub < p1; p += 2 * kStep) {
+    round(p, 0);
+    if (p + kStep - kSelAhead * sub < p1) round(p + kStep, 1);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // Shared memory of the choice.
 struct Chooser {
   unsigned bins[256];
-  uint4 sums[2][kSelWarps / 4];  // one value per warp, two sets
+  uint4 sums[2];                 // one value per warp, two sets
   unsigned digit, above, count;
 };
 
 // One value per warp (the same in all its lanes) to every thread, joined by `join`; one barrier.
 template <typename F>
 __device__ __forceinline__ unsigned block_join(unsigned v, uint4* buf, F join) {
-  static_assert(kSelWarps == 8, "two 16-byte reads");
+  static_assert(kSelWarps == 4, "one 16-byte read");
   if ((threadIdx.x & 31) == 0) reinterpret_cast<unsigned*>(buf)[threadIdx.x >> 5] = v;
   __syncthreads();
-  const uint4 x = buf[0], y = buf[1];
-  return join(join(join(x.x, x.y), join(x.z, x.w)), join(join(y.x, y.y), join(y.z, y.w)));
+  const uint4 x = *buf;
+  return join(join(x.x, x.y), join(x.z, x.w));
 }
 // The sum of the warps before this one.
 __device__ __forceinline__ unsigned block_before(unsigned v, uint4* buf) {
@@ -250,9 +276,9 @@ __device__ void take_largest(const uint32_t* keys, int m, int k, int base, int32
     top = max(top, x);
     low = min(low, x);
   }
-  s.bins[tid] = 0u;
-  top = block_join(__reduce_max_sync(kFull, top), s.sums[0], [](unsigned x, unsigned y) { return max(x, y); });
-  low = block_join(__reduce_min_sync(kFull, low), s.sums[1], [](unsigned x, unsigned y) { return min(x, y); });
+  s.bins[2 * tid] = s.bins[2 * tid + 1] = 0u;
+  top = block_join(__reduce_max_sync(kFull, top), &s.sums[0], [](unsigned x, unsigned y) { return max(x, y); });
+  low = block_join(__reduce_min_sync(kFull, low), &s.sums[1], [](unsigned x, unsigned y) { return min(x, y); });
   int shift = 32 - __clz(top ^ low);  // bits below the ones all keys share
   uint32_t T = shift == 32 ? 0u : top >> shift << shift;
   unsigned want = k;                  // of the keys that agree with T above `shift`
@@ -267,20 +293,23 @@ __device__ void take_largest(const uint32_t* keys, int m, int k, int base, int32
       if ((high == 32 ? 0u : x >> high) == prefix) atomicAdd(&s.bins[x >> shift & mask], 1u);
     }
     __syncthreads();
-    const unsigned mine = s.bins[255 - tid];  // bins from the highest on
-    unsigned upto = mine;
+    const int d1 = 255 - 2 * tid;  // bins d1 and d1 - 1: from the highest on
+    const unsigned m1 = s.bins[d1], m0 = s.bins[d1 - 1];
+    unsigned upto = m1 + m0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned v = __shfl_up_sync(kFull, upto, o);
       if (lane >= o) upto += v;
     }
-    upto += block_before(__shfl_sync(kFull, upto, 31), s.sums[0]);
-    if (upto >= want && upto - mine < want) {
-      s.digit = 255 - tid;
-      s.above = upto - mine;
-      s.count = mine;
+    upto += block_before(__shfl_sync(kFull, upto, 31), &s.sums[0]);
+    const unsigned before1 = upto - m0 - m1, before0 = upto - m0;
+    if (upto >= want && before1 < want) {
+      const bool first = before0 >= want;
+      s.digit = first ? d1 : d1 - 1;
+      s.above = first ? before1 : before0;
+      s.count = first ? m1 : m0;
     }
-    s.bins[255 - tid] = 0u;  // (each thread's own) for the next round
+    s.bins[d1] = s.bins[d1 - 1] = 0u;  // (each thread's own) for the next round
     __syncthreads();
     T |= s.digit << shift;
     want -= s.above;
@@ -302,12 +331,12 @@ __device__ void take_largest(const uint32_t* keys, int m, int k, int base, int32
   }
   unsigned out, tie;
   if (m < 65536) {  // both counts in one exchange
-    const unsigned before = block_before(__reduce_add_sync(kFull, gt << 16 | eq), s.sums[0]);
+    const unsigned before = block_before(__reduce_add_sync(kFull, gt << 16 | eq), &s.sums[0]);
     out = before >> 16;
     tie = before & 0xffffu;
   } else {
-    out = block_before(__reduce_add_sync(kFull, gt), s.sums[0]);
-    tie = block_before(__reduce_add_sync(kFull, eq), s.sums[1]);
+    out = block_before(__reduce_add_sync(kFull, gt), &s.sums[0]);
+    tie = block_before(__reduce_add_sync(kFull, eq), &s.sums[1]);
   }
   if (!exact) out += min(tie, want);
   const unsigned below = (1u << lane) - 1u;
@@ -324,10 +353,12 @@ __device__ void take_largest(const uint32_t* keys, int m, int k, int base, int32
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kSelThreads, 4) select_pages_kernel(Geom g, SelectArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 6) select_pages_kernel(Geom g, SelectArgs a) {
   __shared__ float W[2 * kD];
   __shared__ Chooser chooser;
-  __shared__ __align__(16) uint32_t own_keys[kSelKeys];
+  __shared__ uint32_t local_keys[kLocalKeys];
+  extern __shared__ __align__(16) uint8_t ring[];
+  uint32_t* all_keys = reinterpret_cast<uint32_t*>(ring);  // in the ring's place, once all scores are there
   __shared__ int last;
   const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int64_t grp = (int64_t)b * g.H + h;
@@ -346,12 +377,12 @@ __global__ void __launch_bounds__(kSelThreads, 4) select_pages_kernel(Geom g, Se
     return;
   }
   const int lo = a.sink, hi = n - a.recent, m = hi - lo, k = a.budget - a.sink - a.recent;
-  const bool local = a.nsplit == 1 && m <= kSelKeys;  // the keys never leave shared memory
-  uint32_t* keys = local ? own_keys : a.keys + grp * g.maxp;
+  const bool local = a.nsplit == 1 && m <= kLocalKeys;  // the keys never leave shared memory
+  uint32_t* keys = local ? local_keys : a.keys + grp * g.maxp;
   if (k > 0) {
     const int per = (m + a.nsplit - 1) / a.nsplit;
     const int p0 = min(hi, lo + split * per), p1 = min(hi, p0 + per);
-    if (p0 < p1) score_pages<BF16>(g, a.q, a.Gq, a.bounds, b, h, p0, p1, lo, keys, W);
+    if (p0 < p1) score_pages<BF16>(g, a.q, a.Gq, a.bounds, b, h, p0, p1, lo, keys, W, ring);
   }
   if (a.nsplit > 1) {
     __threadfence();
@@ -363,13 +394,16 @@ __global__ void __launch_bounds__(kSelThreads, 4) select_pages_kernel(Geom g, Se
     __syncthreads();
     if (!last) return;
     __threadfence();
-    if (m <= kSelKeys && k > 0) {
-      for (int i = threadIdx.x; i < m; i += kSelThreads) own_keys[i] = __ldcg(keys + i);
-    }
+  } else {
+    __syncthreads();
   }
-  __syncthreads();
+  const bool fits = !local && m <= kSelKeys;
+  if (fits && k > 0) {
+    for (int i = threadIdx.x; i < m; i += kSelThreads) all_keys[i] = __ldcg(keys + i);
+    __syncthreads();
+  }
   if (k > 0) {
-    if (m <= kSelKeys) take_largest<false>(own_keys, m, k, lo, list + a.sink, chooser);
+    if (local || fits) take_largest<false>(local ? local_keys : all_keys, m, k, lo, list + a.sink, chooser);
     else take_largest<true>(keys, m, k, lo, list + a.sink, chooser);
   }
   for (int i = threadIdx.x; i < a.sink; i += kSelThreads) list[i] = i;
@@ -400,12 +434,23 @@ cudaError_t launch_select(const Geom& g, SelectArgs a, void* ws, int num_sms, cu
   const size_t groups = (size_t)g.B * g.H;
   a.arrivals = (int*)ws;
   a.keys = (uint32_t*)((uint8_t*)ws + (groups * sizeof(int) + 255) / 256 * 256);
-  // four CTAs per SM, each with 64 pages (one round of its warps) or more
-  const int64_t most = std::max(1, g.maxp / 64);
-  a.nsplit = (int)std::min<int64_t>(most, std::max<int64_t>(1, 4 * (int64_t)num_sms / (int64_t)groups));
+  // as many CTAs as six per SM, each with 32 pages (one round of its warps) or more
+  const int64_t most = std::max(1, g.maxp / 32);
+  a.nsplit = (int)std::min<int64_t>(most, std::max<int64_t>(1, 6 * (int64_t)num_sms / (int64_t)groups));
   const dim3 grid(a.nsplit, g.H, g.B);
-  if (g.dtype == KVQ_BF16) select_pages_kernel<true><<<grid, kSelThreads, 0, st>>>(g, a);
-  else select_pages_kernel<false><<<grid, kSelThreads, 0, st>>>(g, a);
+  auto* kernel = g.dtype == KVQ_BF16 ? select_pages_kernel<true> : select_pages_kernel<false>;
+  // the kernel's shared-memory limit is raised once per device
+  static std::atomic<bool> raised[2][64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int bf = g.dtype == KVQ_BF16;
+  if (dev < 0 || dev >= 64 || !raised[bf][dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelRing);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) raised[bf][dev].store(true, std::memory_order_relaxed);
+  }
+  kernel<<<grid, kSelThreads, kSelRing, st>>>(g, a);
   return cudaGetLastError();
 }
 
