@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -61,7 +62,8 @@ class kvq_rows(ctypes.Structure):
 
 
 _P = ctypes.POINTER(kvq_cache)
-_R = ctypes.POINTER(kvq_rows)
+_pack_rows = struct.Struct("PPPiiqqqq").pack  # the bytes of a kvq_rows
+assert struct.calcsize("PPPiiqqqq") == ctypes.sizeof(kvq_rows)
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _SIGS = {
     "kvq_page_bytes": (_sz, [_P]),
@@ -77,7 +79,7 @@ _SIGS = {
     "kvq_decode_attention_static": (ctypes.c_int, [_P, _vp, _i32, _f32, _vp, _vp]),
     "kvq_step_workspace_bytes": (_sz, [_P, _i32]),
     "kvq_decode_step": (ctypes.c_int, [_P, _vp, _vp, _vp, _i32, _f32, _vp, _vp, _sz, _vp]),
-    "kvq_norm_rope": (ctypes.c_int, [_R, _R, _R, _i32, _i64, _vp, _vp, _i32, _i32, _f32, _vp]),
+    "kvq_norm_rope": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _vp, _vp, _i32, _i32, _f32, _vp]),
     "kvq_plan_workspace_bytes": (_sz, [_P]),
     "kvq_plan_pages": (ctypes.c_int, [_P, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
     "kvq_page_bounds": (ctypes.c_int, [_P, _vp, _i32, _vp, _vp]),
@@ -230,9 +232,10 @@ def _ws(ws: torch.Tensor | None, dev: int) -> tuple[int | None, int]:
     return ws.data_ptr(), ws.nbytes
 
 
-def _rows(name: str, x: torch.Tensor | None, out: torch.Tensor | None, weight: torch.Tensor | None, dtype, tokens: int, dev: int) -> kvq_rows:
+def _rows(name: str, x: torch.Tensor | None, out: torch.Tensor | None, weight: torch.Tensor | None, dtype, tokens: int, dev: int) -> bytes | None:
+    """The bytes of a kvq_rows (None: no rows)."""
     if x is None:
-        return kvq_rows()
+        return None
     if out is None:
         raise KvqError(KVQ_ERR_INVALID_ARG, f"{name} has no output")
     shape, xs, os_ = x.shape, x.stride(), out.stride()
@@ -242,8 +245,8 @@ def _rows(name: str, x: torch.Tensor | None, out: torch.Tensor | None, weight: t
                        f"CUDA device, got {x.dtype} {list(shape)} {list(xs)} on {x.device} and {out.dtype} {list(out.shape)} {list(os_)} on {out.device}")
     # the stride of a dimension of one element is never used, whatever it says
     one_t, one_h = tokens == 1, shape[1] == 1
-    return kvq_rows(x.data_ptr(), out.data_ptr(), None if weight is None else _want(name + "_weight", weight, dtype, (HEAD_DIM,), dev),
-                    shape[1], 0, 0 if one_t else xs[0], 0 if one_h else xs[1], 0 if one_t else os_[0], 0 if one_h else os_[1])
+    return _pack_rows(x.data_ptr(), out.data_ptr(), 0 if weight is None else _want(name + "_weight", weight, dtype, (HEAD_DIM,), dev),
+                      shape[1], 0, 0 if one_t else xs[0], 0 if one_h else xs[1], 0 if one_t else os_[0], 0 if one_h else os_[1])
 
 
 def kvq_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None, positions: torch.Tensor | None,
