@@ -786,9 +786,9 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
     // thread = channel; each M_V value is read once per CTA
     {
       const int c = threadIdx.x;
-      float o[NH];
+      unsigned long long o2[NH / 2];  // two heads at a time
 #pragma unroll
-      for (int i = 0; i < NH; ++i) o[i] = 0.f;
+      for (int i = 0; i < NH / 2; ++i) o2[i] = 0ull;
       for (int j0 = 0; j0 < Pe; j0 += kMvAhead) {
         if (j0 > 0) {
 #pragma unroll
@@ -797,11 +797,20 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 #pragma unroll
         for (int j = 0; j < kMvAhead; ++j) {
           if (j0 + j < Pe) {
+            const ulonglong2* w = reinterpret_cast<const ulonglong2*>(wc + (j0 + j) * NH);
+            const unsigned long long m2 = pk(mval[j], mval[j]);
 #pragma unroll
-            for (int i = 0; i < NH; ++i) o[i] = fmaf(wc[(j0 + j) * NH + i], mval[j], o[i]);
+            for (int i = 0; i < NH / 4; ++i) {
+              const ulonglong2 x = w[i];
+              o2[2 * i] = fma2(x.x, m2, o2[2 * i]);
+              o2[2 * i + 1] = fma2(x.y, m2, o2[2 * i + 1]);
+            }
           }
         }
       }
+      float o[NH];
+#pragma unroll
+      for (int i = 0; i < NH / 2; ++i) upk(o2[i], o[2 * i], o[2 * i + 1]);
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
         if (i >= Gq) break;
@@ -923,7 +932,7 @@ int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms) {
   auto round = [&](int64_t k, int pages) { return 5.0 + 1.25 * (k - 1) + pages * std::max(1.0, 0.48 * k); };
   int best = least;
   double best_cost = 1e300;
-  for (int ns = least; ns <= most; ++ns) {
+  for (int ns = least; ns <= most; ns += std::max(1, ns / 8)) {
     const int64_t per_sm = (units * ns + sms - 1) / sms, full = per_sm / occ, rem = per_sm % occ;
     const int pages = ((budget + ns - 1) / ns + kNW - 1) / kNW;
     const double cost = full * round(occ, pages) + (rem ? round(rem, pages) : 0.0) + 0.05 * ns;
