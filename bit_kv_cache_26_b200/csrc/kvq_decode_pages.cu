@@ -119,7 +119,7 @@ __host__ __device__ inline PagesSmem pages_smem(int sub_bytes, int NT, bool wide
   s.t_row = banked(P, wide ? 4 : 8);
   s.w_row = banked(P + 1, wide ? 4 : 8);  // +1: tokens stored raw
   // the ring; the merge at the end reuses its place
-  const int merge = (kNW * NH * kD + 3 * kNW * NH + kNW * NH * 4 + P * NH + NH * kNW + NH * kD + NH) * 4;
+  const int merge = (kNW * NH * kD + 3 * kNW * NH + kNW * NH * 4 + P * NH + NH * kNW + NH * kD + 2 * NH) * 4;
   int o = max(kNW * kStages * sub_bytes, merge);
   o = (o + 15) & ~15;
   s.bars = o; o += kNW * kStages * 8;
@@ -134,6 +134,30 @@ __host__ __device__ inline PagesSmem pages_smem(int sub_bytes, int NT, bool wide
   if (!wide) s.qk = s.W + NH * kD * 4;
   s.total = o;
   return s;
+}
+
+// All threads of the cluster: shared memory written before is seen by the others after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+// Shared memory of the CTA of rank r of the cluster, at the place of p in this one's.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, int r) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(r));
+  return a;
+}
+__device__ __forceinline__ float2 peer_f2(const void* p, int r) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer_addr(p, r)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_f4(const void* p, int r) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer_addr(p, r))
+               : "memory");
+  return v;
 }
 
 // Output of one query head from its channels 4 lane .. 4 lane + 3 of sum p v and its sum p.
@@ -227,6 +251,11 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
   const int Pe = p_eff(g, (int)sh);
   const float* MK = g.kpat + sh * P * kD;
   const int64_t row0 = ((int64_t)b * a.Hq + (int64_t)h * Gq) * a.nsplit + split;  // partial row of head 0; + hh * nsplit
+
+  // a group's sums, when they are merged in shared memory: [NH][128] sum p v and [NH] (max, sum p), after the merge's places
+  const bool in_smem = a.nsplit == 1 || a.clustered;
+  float* sum_o = reinterpret_cast<float*>(smem) + kNW * NH * kD + 3 * kNW * NH + kNW * NH * 4 + P * NH + NH * kNW;
+  float2* sum_ml = reinterpret_cast<float2*>(sum_o + NH * kD);
 
   if (n_mine > 0) {
     // the first of the setup's loads go out before the page copies, which would keep them waiting: this warp's
@@ -735,7 +764,6 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
     float* munit = mz + kNW * NH * 4;            // [kNW][NH] unit of the pattern weights
     float* wc = munit + kNW * NH;                // [P][NH] merged pattern weights
     float* fsh = wc + P * NH;                    // [NH][kNW] warp weights
-    float* ol = fsh + NH * kNW;                  // [NH][128] sum p v, then [NH] sum p (one split)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -772,8 +800,8 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         if (lane == w) fsh[hh * kNW + w] = f[w];
       }
       if (lane == 0) {
-        if (a.nsplit > 1) reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(M, Ls);
-        else ol[NH * kD + hh] = M == -INFINITY ? 0.f : Ls;
+        if (in_smem) sum_ml[hh] = make_float2(M, Ls);
+        else reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(M, Ls);
       }
       for (int jj = lane; jj < Pe; jj += 32) {
         float s = 0.f;
@@ -817,28 +845,50 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 #pragma unroll
         for (int w = 0; w < kNW; ++w)
           o[i] = fmaf(fsh[i * kNW + w], mo[(w * NH + i) * kD + c] + mz[(w * NH + i) * 4 + (c >> 5)], o[i]);
-        if (a.nsplit > 1) a.part_o[(row0 + (int64_t)i * a.nsplit) * kD + c] = o[i];
-        else ol[i * kD + c] = o[i];
+        if (in_smem) sum_o[i * kD + c] = o[i];
+        else a.part_o[(row0 + (int64_t)i * a.nsplit) * kD + c] = o[i];
       }
     }
-    if (a.nsplit == 1) {  // the only split: straight to the output
-      __syncthreads();
-      for (int hh = warp; hh < Gq; hh += kNW) {
-        float o[4], l = ol[NH * kD + hh];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = l == 0.f ? 0.f : ol[hh * kD + 4 * lane + k];
-        finish_head(g, o, l == 0.f ? 1.f : l, g.vcol + sh * kD, a.out + ((int64_t)b * a.Hq + (int64_t)h * Gq + hh) * kD, lane);
-      }
-      return;
-    }
-  } else if (a.nsplit == 1) {  // no entries
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + ((int64_t)b * a.Hq + (int64_t)h * Gq) * kD);
-    for (int i = threadIdx.x; i < Gq * kD / 2; i += blockDim.x) out[i] = 0u;
-    return;
   } else {
     // nothing of the list falls to this CTA
-    for (int hh = threadIdx.x; hh < Gq; hh += blockDim.x)
-      reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(-INFINITY, 0.f);
+    for (int hh = threadIdx.x; hh < Gq; hh += blockDim.x) {
+      if (in_smem) sum_ml[hh] = make_float2(-INFINITY, 0.f);
+      else reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(-INFINITY, 0.f);
+    }
+  }
+
+  // ---- one split, or a cluster of them: the sums stay in shared memory, and CTA r of the group finishes heads r, r + nsplit, ...
+  if (in_smem) {
+    if (a.nsplit > 1) cluster_sync(); else __syncthreads();
+    for (int hh = split + a.nsplit * warp; hh < Gq; hh += a.nsplit * kNW) {
+      float2 x = make_float2(-INFINITY, 0.f);
+      if (lane < a.nsplit) x = a.nsplit > 1 ? peer_f2(sum_ml + hh, lane) : sum_ml[hh];
+      const float M = warp_max(x.x);
+      float Ls = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+      if (M > -INFINITY) {
+        const float fs = x.x == -INFINITY ? 0.f : ex2(x.x - M);
+        Ls = warp_sum(fs * x.y);
+        const float* row = sum_o + hh * kD + 4 * lane;
+        for (int i0 = 0; i0 < a.nsplit; i0 += 8) {
+          float4 y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            y[i] = a.nsplit > 1 ? peer_f4(row, min(i0 + i, a.nsplit - 1)) : *reinterpret_cast<const float4*>(row);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            // (a split without entries has written no row: its weight is 0, whatever is read; so past the last one)
+            const float f = __shfl_sync(kFull, fs, i0 + i);
+            o[0] += f == 0.f ? 0.f : f * y[i].x;
+            o[1] += f == 0.f ? 0.f : f * y[i].y;
+            o[2] += f == 0.f ? 0.f : f * y[i].z;
+            o[3] += f == 0.f ? 0.f : f * y[i].w;
+          }
+        }
+      }
+      finish_head(g, o, M > -INFINITY ? Ls : 1.f, g.vcol + sh * kD, a.out + ((int64_t)b * a.Hq + (int64_t)h * Gq + hh) * kD, lane);
+    }
+    if (a.nsplit > 1) cluster_sync();  // the others' reads of this CTA's sums are done
+    return;
   }
 
   // ---- the CTA that completes a group merges its splits and writes the output
@@ -903,8 +953,22 @@ cudaError_t launch_one(const Geom& g, const PagesArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) allowed[dev].store(kMaxSmem, std::memory_order_relaxed);
   }
-  decode_pages_kernel<BITS, NT, WIDE><<<dim3(a.nsplit, g.H, g.B), kNW * 32, smem, st>>>(g, a);
-  return cudaGetLastError();
+  if (!a.clustered) {
+    decode_pages_kernel<BITS, NT, WIDE><<<dim3(a.nsplit, g.H, g.B), kNW * 32, smem, st>>>(g, a);
+    return cudaGetLastError();
+  }
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = a.nsplit;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.nsplit, g.H, g.B);
+  cfg.blockDim = dim3(kNW * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_pages_kernel<BITS, NT, WIDE>, g, a);
 }
 
 template <int BITS>
@@ -916,11 +980,12 @@ cudaError_t launch_bits(const Geom& g, const PagesArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Splits of the list.  Model, in units of the time a lone CTA takes for a page per warp (1.3 us on one B200): k CTAs on an
-// SM at once take max(1, 0.48 k) for a page per warp and 5 + 1.25 (k - 1) before and after the loop; the busiest SM runs
-// its CTAs `occ` at a time; merging costs a little per split.  At most kWarpEntries entries per warp.  Measured at 64
-// listed pages of 4 bits for 8 groups (best 16 splits, 13.7 us; 1: 30 us; 64: 28 us), for 64 groups (best 4), at 256 pages
-// for 8 groups (best 16), at 128 pages for 256 groups (best 2) and 2048 (1).
+// Splits of the list: 1, 2, 4 or 8 (a cluster, whose sums meet in shared memory), or 16 and more (through the workspace).
+// Model, in units of the time a lone CTA takes for a page per warp (1.3 us on one B200): k CTAs on an SM at once take
+// max(1, 0.48 k) for a page per warp and 5 + 1.25 (k - 1) before and after the loop; the busiest SM runs its CTAs `occ` at a
+// time; merging costs a little per split.  At most kWarpEntries entries per warp.  Measured (through the workspace) at 64
+// listed pages of 4 bits for 8 groups (best 16 splits, 12.7 us; 1: 29 us; 64: 23 us), for 64 groups (best 4), at 256 pages
+// for 8 groups (best 16), at 128 pages for 256 groups (best 2) and 2048 (1).  These are the model's choices.
 int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms) {
   const int64_t units = std::max<int64_t>(1, (int64_t)g.B * g.H), sms = std::max(1, num_sms);
   const bool wide = Gq > 4;
@@ -932,7 +997,8 @@ int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms) {
   auto round = [&](int64_t k, int pages) { return 5.0 + 1.25 * (k - 1) + pages * std::max(1.0, 0.48 * k); };
   int best = least;
   double best_cost = 1e300;
-  for (int ns = least; ns <= most; ns += std::max(1, ns / 8)) {
+  for (int ns = 1; ns <= most; ns = ns < 16 ? 2 * ns : ns + ns / 8) {
+    if (ns < least) continue;
     const int64_t per_sm = (units * ns + sms - 1) / sms, full = per_sm / occ, rem = per_sm % occ;
     const int pages = ((budget + ns - 1) / ns + kNW - 1) / kNW;
     const double cost = full * round(occ, pages) + (rem ? round(rem, pages) : 0.0) + 0.05 * ns;
@@ -951,6 +1017,9 @@ size_t decode_pages_workspace(const Geom& g, int Hq, int nsplit) {
 cudaError_t launch_decode_pages(const Geom& g0, PagesArgs a, void* ws, cudaStream_t st) {
   Geom g = g0;
   g.wait_limit = page_wait_limit(g0.wait_limit);
+  // 64 groups of 64 pages, 4 splits: 17.1 us as clusters, 20.8 us through the workspace; 8 groups, 8 splits: 11.1 / 13.6 us;
+  // 16 splits measured the same either way
+  a.clustered = a.nsplit == 2 || a.nsplit == 4 || a.nsplit == 8;
   a.arrivals = (int*)ws;
   a.part_ml = (float*)((uint8_t*)ws + counters_bytes(g));
   a.part_o = a.part_ml + 2 * (size_t)g.B * a.Hq * a.nsplit;

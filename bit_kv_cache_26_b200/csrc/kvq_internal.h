@@ -41,7 +41,7 @@ struct PagesArgs {
   float scale_log2;
   const int32_t* list;      // [B][H][budget]
   const int32_t* list_len;  // [B][H]
-  int budget, nsplit;
+  int budget, nsplit, clustered;
   uint16_t* out;
   float* part_ml;
   float* part_o;

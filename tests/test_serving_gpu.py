@@ -446,6 +446,7 @@ def attend(cache, q, lists, n, scale=None, ws=None, **kw):
     ("bf16", 4, 1, 2, 7, 8, [321, 64, 1], 6), ("fp16", 2, 1, 1, 7, 30, [1000, 999], 32), ("fp16", 4, 0, 1, 16, 255, [513, 512], 17),
     ("bf16", 2, 0, 3, 12, 100, [250, 640, 31], 8), ("bf16", 4, 0, 8, 4, 64, [5000], 64), ("fp16", 2, 0, 4, 2, 17, [2100] * 5, 33),
     ("bf16", 2, 0, 2, 5, 33, [4000] * 2, 126), ("fp16", 4, 1, 1, 9, 64, [3000, 40], 50),
+    ("bf16", 4, 0, 1, 4, 64, [40007], 1251), ("fp16", 2, 0, 1, 8, 16, [9000, 8000], 6000), ("bf16", 2, 1, 1, 16, 255, [4001], 126),
 ])
 def test_attention_over_pages(kvq, dtype, bits, tx, H, Gq, P, lengths, budget):
     dt = DT[dtype]
