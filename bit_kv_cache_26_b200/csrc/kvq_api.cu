@@ -318,7 +318,7 @@ kvq_status kvq_plan_pages(const kvq_cache* cache, const int32_t* new_len, const 
   if (!aligned(ws, 4)) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 4-byte aligned");
   kvq::PlanArgs a{new_len,  free_pages, free_capacity, free_count, free_left, cu_new,
                   slot_map, positions,  seq_ids,       max_tokens, (int32_t*)ws};
-  cudaError_t e = kvq::launch_plan(g, a, (cudaStream_t)stream);
+  cudaError_t e = kvq::launch_plan(g, a, num_sms(), (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "kvq_plan_pages");
   return KVQ_OK;
 }

@@ -14,6 +14,10 @@
 //   W: the query heads in 16 places (absent ones 0), halved: places i and i + 8, + 4, + 2, + 1;
 //   term_d = fl(fl(W+_d hi_d) + fl(W-_d lo_d)); 8 neighbouring channels halved (4, 2, 1), then
 //   the 16 sums halved (8, 4, 2, 1).  Equal scores: the lower page.  NaN ranks above all.
+//
+// Bound: HBM.  One B200: bounds of 8 x 32768 keys x 8 heads 94 us (6.1 TB/s, 0.93 of the copy
+// bandwidth); selection over 256 sequences x 8 heads x 512 pages 99 us (5.4 TB/s, 0.83), for one
+// sequence of 1024 pages 11 us of latency (lengths, page ids, bounds, the last CTA's choice).
 #include <algorithm>
 #include <atomic>
 

@@ -1,5 +1,11 @@
 // Decode attention over chosen pages of the quantized paged cache: per (sequence, KV head) a list
-// of pages, softmax(q . K_hat^T) V_hat over their tokens only, in the cache's 2- or 4-bit codes.
+// of pages, softmax(q . K_hat^T) V_hat over their tokens only, in the cache's 2- or 4-bit codes
+// ("PatternKV", Section 3.4: the fused reconstruction and attention, over a subset of the pages).
+//
+// Bound: the listed sub-blocks from HBM.  One B200, 256 sequences x 8 KV heads x 128 of 512 pages in
+// 4 bits, 4 query heads each: 330 us, 4.9 TB/s of page bytes (0.75 of the copy bandwidth; the loop
+// alone streams at about 0.9, the rest is each CTA's setup and merge).  Before: pattern weights by
+// turn-taking in shared memory and both columns' products formed by both lanes, 481 us.
 //
 // Per CTA one (sequence, KV head, split of the list); each warp streams its entries' sub-blocks
 // through a ring of shared-memory stages (cp.async.bulk, bounded mbarrier waits).
@@ -221,9 +227,9 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
   // entries of this warp: split + nsplit (warp + kNW i).  Lane l of window w reads entry i = 32 w + l; the first
   // window goes out with the lengths.
   const int32_t* list = a.list + grp * a.budget;
-  const int stride = a.nsplit * kNW, e_first = split + a.nsplit * warp;
+  const int64_t stride = (int64_t)a.nsplit * kNW, e_first = split + (int64_t)a.nsplit * warp;
   auto entry = [&](int i) -> int {
-    const int64_t e = e_first + (int64_t)stride * i;
+    const int64_t e = e_first + stride * i;
     return e < a.budget ? __ldg(list + e) : -1;
   };
   int lp = entry(lane);
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
   }
   const int nfull = L / kG, ntail = L % kG, npages = nfull + (ntail > 0);
   // this CTA's entries: split, split + nsplit, ... (dealt so that the list can be read before its length is known)
-  const int n_mine = (n_list - split + a.nsplit - 1) / a.nsplit;
+  const int n_mine = (int)(((int64_t)n_list - split + a.nsplit - 1) / a.nsplit);
   const size_t sh = (size_t)set * g.H + h;
   const int Pe = p_eff(g, (int)sh);
   const float* MK = g.kpat + sh * P * kD;

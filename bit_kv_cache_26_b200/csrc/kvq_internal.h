@@ -82,7 +82,7 @@ struct PlanArgs {
   int32_t* ws;
 };
 size_t plan_workspace(const Geom& g);
-cudaError_t launch_plan(const Geom& g, const PlanArgs& a, cudaStream_t st);
+cudaError_t launch_plan(const Geom& g, const PlanArgs& a, int num_sms, cudaStream_t st);
 
 // norms and rotation (kvq_rope.cu)
 struct RopeRows {

@@ -5,6 +5,11 @@
 // in the packed order and every new page its place on the free stack, whose top is taken first.
 // A sequence is served when the scans up to and including it stay within the slot map and the
 // stack; both scans only grow, so the served ones are those before the first that does not fit.
+//
+// Bound: latency for a decode step (256 sequences of one token: 4.5 us on one B200), 16 bytes written
+// per token for prompts (256 of up to 16384 tokens, 3.1 M in all: 15.6 us, 3.3 TB/s; every CTA's scan
+// before its first store is a fifth of it).  Two launches, the scan and the expansion, took 17 us there
+// and 7.2 us for the decode step.
 #include <algorithm>
 
 #include "kvq_common.cuh"
@@ -16,8 +21,8 @@ namespace {
 
 constexpr int kPlanThreads = 256;
 constexpr int kPlanOnce = 2048;       // up to so many sequences every CTA makes the scans for itself: one launch
-constexpr int kPlanItems = kPlanOnce / kPlanThreads;
-constexpr int64_t kOnceTokens = 1 << 19;  // and so many tokens (512 CTAs: beyond, making the scans once is faster)
+constexpr int kOnceCtas = 4;          // CTAs per SM then, at most
+constexpr int kPlanAhead = 2;         // rounds of a chunk (two tokens per thread each)
 constexpr int kPlanScan = 1024;       // threads of the scan when it is a launch of its own
 
 __device__ __forceinline__ longlong2 add2ll(longlong2 a, longlong2 b) { return make_longlong2(a.x + b.x, a.y + b.y); }
@@ -52,6 +57,34 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int i, int lo, int hi) 
 // sequences before) and len: in shared or global memory.
 __device__ __forceinline__ void expand(const Geom& g, const PlanArgs& a, const int32_t* cu, const int32_t* before,
                                        const int32_t* len, int begin, int end, int s_lo, int s_hi, int free_n) {
+  if (s_lo == s_hi && end - begin == 2 * kPlanThreads * kPlanAhead) {
+    // the whole chunk in one sequence, as in a long prompt: the page ids of all rounds first, then the stores
+    const int s = s_lo, L = len[s], held = (L + kG - 1) / kG, top = free_n - 1 - (before[s] - held);
+    const int pos0 = L + (begin - cu[s]) + 2 * (int)threadIdx.x;
+    int32_t* row = const_cast<int32_t*>(g.page_table) + (int64_t)s * g.maxp;
+    auto page_id = [&](int pos) {
+      const int p = pos / kG;
+      return p < held ? row[p] : a.free_pages[top - p];
+    };
+    int id0[kPlanAhead], id1[kPlanAhead];
+#pragma unroll
+    for (int u = 0; u < kPlanAhead; ++u) {
+      const int pos = pos0 + 2 * kPlanThreads * u;
+      id0[u] = page_id(pos);
+      id1[u] = (pos + 1) % kG == 0 ? page_id(pos + 1) : id0[u];
+    }
+#pragma unroll
+    for (int u = 0; u < kPlanAhead; ++u) {
+      const int pos = pos0 + 2 * kPlanThreads * u, i0 = begin + 2 * (int)threadIdx.x + 2 * kPlanThreads * u;
+      *reinterpret_cast<int2*>(a.positions + i0) = make_int2(pos, pos + 1);
+      *reinterpret_cast<int2*>(a.seq_ids + i0) = make_int2(s, s);
+      *reinterpret_cast<longlong2*>(a.slot_map + i0) =
+          make_longlong2((int64_t)id0[u] * kG + pos % kG, (int64_t)id1[u] * kG + (pos + 1) % kG);
+      if (pos % kG == 0) row[pos / kG] = id0[u];
+      if ((pos + 1) % kG == 0) row[(pos + 1) / kG] = id1[u];
+    }
+    return;
+  }
   for (int i0 = begin + 2 * (int)threadIdx.x; i0 < end; i0 += 2 * kPlanThreads) {
     int s = seq_of(cu, i0, s_lo, s_hi), base = -1, next = -1, L = 0, held = 0, page = -1, phys = 0;
     int pos[2], ids[2];
@@ -91,11 +124,12 @@ __device__ __forceinline__ void expand(const Geom& g, const PlanArgs& a, const i
   }
 }
 
-// One launch: every CTA scans all requests (eight consecutive ones per thread) into shared memory and writes its chunk of
+// One launch: every CTA scans all requests (consecutive ones per thread) into shared memory and writes its chunk of
 // the tokens; the first also writes cu_new, and the last one to have read the free count writes what is left of it
 // (which may be the same word).  Workspace: [0] counts the CTAs that have read it, back to 0 at the end.
+template <int ITEMS>  // requests per thread, at most
 __global__ void __launch_bounds__(kPlanThreads) plan_once_kernel(Geom g, PlanArgs a, int chunk) {
-  __shared__ int32_t cu[kPlanOnce + 1], before[kPlanOnce], len[kPlanOnce];
+  __shared__ int32_t cu[kPlanThreads * ITEMS + 1], before[kPlanThreads * ITEMS], len[kPlanThreads * ITEMS];
   __shared__ longlong2 warp_tot[kPlanThreads / 32];
   __shared__ longlong2 s_tot;
   __shared__ int s_free, s_last, s_range[2];
@@ -107,9 +141,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_once_kernel(Geom g, PlanArg
     s_last = atomicInc(reinterpret_cast<unsigned*>(a.ws), gridDim.x - 1) == gridDim.x - 1;
   }
   const int items = (g.B + kPlanThreads - 1) / kPlanThreads, b0 = tid * items;
-  longlong2 mine[kPlanItems], sum = make_longlong2(0, 0);
+  longlong2 mine[ITEMS], sum = make_longlong2(0, 0);
 #pragma unroll
-  for (int i = 0; i < kPlanItems; ++i) {
+  for (int i = 0; i < ITEMS; ++i) {
     mine[i] = make_longlong2(0, 0);
     const int b = b0 + i;
     if (i < items && b < g.B) {
@@ -129,7 +163,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_once_kernel(Geom g, PlanArg
   int n_mine = 0;  // served ones of them: the sums only grow, so the first
   longlong2 end = at;
 #pragma unroll
-  for (int i = 0; i < kPlanItems; ++i) {
+  for (int i = 0; i < ITEMS; ++i) {
     const int b = b0 + i;
     if (i < items && b < g.B) {
       const longlong2 next = add2ll(at, mine[i]);
@@ -151,7 +185,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_once_kernel(Geom g, PlanArg
   __syncthreads();
   const longlong2 tot = s_tot;
 #pragma unroll
-  for (int i = 0; i < kPlanItems; ++i) {
+  for (int i = 0; i < ITEMS; ++i) {
     const int b = b0 + i;
     if (i < items && b < g.B && i >= n_mine) {
       cu[b + 1] = (int32_t)tot.x;
@@ -163,9 +197,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_once_kernel(Geom g, PlanArg
   if (blockIdx.x == 0)
     for (int b = tid; b <= g.B; b += kPlanThreads) a.cu[b] = cu[b];
   if (tid == 0 && s_last) *a.free_left = (int32_t)(free_n - tot.y);
-  const int64_t begin = (int64_t)blockIdx.x * chunk;
-  if (begin < tot.x) {
+  for (int64_t begin = (int64_t)blockIdx.x * chunk; begin < tot.x; begin += (int64_t)gridDim.x * chunk) {
     const int last = (int)min(tot.x, (long long)(begin + chunk));
+    __syncthreads();  // the range of the chunk before is read
     if (tid < 2) s_range[tid] = seq_of(cu, tid ? last - 1 : (int)begin, 0, g.B - 1);  // the chunk's sequences
     __syncthreads();
     expand(g, a, cu, before, len, (int)begin, last, s_range[0], s_range[1], (int)free_n);
@@ -238,14 +272,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_expand_kernel(Geom g, PlanA
 
 size_t plan_workspace(const Geom& g) { return ((size_t)g.B + 4) * sizeof(int32_t); }
 
-cudaError_t launch_plan(const Geom& g, const PlanArgs& a, cudaStream_t st) {
-  // Measured on one B200, one launch against two: 256 sequences of one token 5.0 / 7.2 us, 2000 of 100 8.7 / 10.5 us,
-  // 32 of 16384 6.2 / 6.6 us, 256 of 4096 10.7 / 8.1 us, 256 of 16384 22 / 17 us.
-  const bool once = g.B <= kPlanOnce && a.max_tokens <= kOnceTokens;
-  const int chunk = once ? 1024 : 2048;  // tokens of a CTA
-  const unsigned grid = (unsigned)std::max<int64_t>(1, (a.max_tokens + chunk - 1) / chunk);
-  if (once) {
-    plan_once_kernel<<<grid, kPlanThreads, 0, st>>>(g, a, chunk);
+cudaError_t launch_plan(const Geom& g, const PlanArgs& a, int num_sms, cudaStream_t st) {
+  constexpr int chunk = 2 * kPlanThreads * kPlanAhead;  // tokens of a CTA at a time
+  const int64_t chunks = std::max<int64_t>(1, (a.max_tokens + chunk - 1) / chunk);
+  if (g.B <= kPlanOnce) {
+    // every CTA makes the scans first, so there are no more than kOnceCtas per SM
+    const unsigned grid = (unsigned)std::min<int64_t>(chunks, (int64_t)kOnceCtas * num_sms);
+    if (g.B <= kPlanThreads) plan_once_kernel<1><<<grid, kPlanThreads, 0, st>>>(g, a, chunk);
+    else plan_once_kernel<kPlanOnce / kPlanThreads><<<grid, kPlanThreads, 0, st>>>(g, a, chunk);
     return cudaGetLastError();
   }
   plan_scan_kernel<<<1, std::min(kPlanScan, (g.B + 127) / 128 * 128), 0, st>>>(g, a);
@@ -255,7 +289,7 @@ cudaError_t launch_plan(const Geom& g, const PlanArgs& a, cudaStream_t st) {
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3((unsigned)chunks);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = st;
   cfg.attrs = &at;
