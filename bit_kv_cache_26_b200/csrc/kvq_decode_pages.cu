@@ -201,7 +201,7 @@ __device__ __forceinline__ void finish_head(const Geom& g, float (&o)[4], float 
 // NT tiles of four query heads (or eight: WIDE).  Thread (gq, tig) of a warp holds the sums of head
 // 4 j + tig of tile j (WIDE: heads 8 j + 2 tig and the next) and forms the B columns of head
 // 4 j + gq / 2 (WIDE: 8 j + gq).
-template <int BITS, int NT, bool WIDE>
+template <int BITS, int NT, bool WIDE, bool TX>
 __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode_pages_kernel(Geom g, PagesArgs a) {
   static_assert(WIDE || NT == 1, "more than four heads: wide tiles");
   constexpr int HPT = WIDE ? 2 : 1, TH = 4 * HPT, NH = NT * TH, WPL = BITS * 4;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
       if (hh > warp) load_q(hh);
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = hh < Gq ? bits_to_float(q_raw[k], g.dtype) : 0.f;
-      if (g.tx) {
+      if constexpr (TX) {
         fwht_warp(v, lane);
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = v[k] * __ldg(g.kcol + sh * kD + lane + 32 * k) * 0.0078125f;
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
       for (int x = 0; x < HPT; ++x) {
         mrun[j][x] = -INFINITY;
         lrun[j][x] = 0.f;
-        vexp[j][x] = g.tx ? -100 : 0;  // (without row factors a weight is at most 1)
+        vexp[j][x] = TX ? -100 : 0;  // (without row factors a weight is at most 1)
         scl[j][x] = a.scale_log2 * qinv[TH * j + HPT * tig + x];
 #pragma unroll
         for (int u = 0; u < 4; ++u) zacc[j][x][u] = 0.f;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
           const float4* kz4 = reinterpret_cast<const float4*>(pgp + g.off_kz) + tig;
           const uint32_t kidx4 = *reinterpret_cast<const uint32_t*>(pgp + g.off_kidx + gq * 4);
           float krow[4] = {1.f, 1.f, 1.f, 1.f};
-          if (g.tx) {
+          if constexpr (TX) {
             const float4 kr = *reinterpret_cast<const float4*>(pgp + g.off_krow + gq * 16);
             krow[0] = kr.x; krow[1] = kr.y; krow[2] = kr.z; krow[3] = kr.w;
           }
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
               for (int u = 0; u < 4; ++u) {
                 const float s = WIDE ? acc[j][u >> 1][2 * (u & 1) + x] : acc[j][u >> 1][2 * (u & 1)] + acc[j][u >> 1][2 * (u & 1) + 1];
                 const int idx = min((int)((kidx4 >> (8 * u)) & 0xff), Pe - 1);
-                sc[j][x][u] = (fmaf(s, u & 1 ? f8 : f0, z) + T[(TH * j + HPT * tig + x) * TR + idx]) * (krow[u] * scl[j][x]);
+                sc[j][x][u] = (fmaf(s, u & 1 ? f8 : f0, z) + T[(TH * j + HPT * tig + x) * TR + idx]) * (TX ? krow[u] * scl[j][x] : scl[j][x]);
               }
             }
           }
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
               reinterpret_cast<float*>(pgp + g.off_vz)[vzc_pos(lane, u)] = 0.f;
             }
             pgp[g.off_vidx + tok_pos(lane)] = (uint8_t)kRawIndex;
-            if (g.tx) reinterpret_cast<float*>(pgp + g.off_vrow)[tok_pos(lane)] = 0.f;
+            if constexpr (TX) reinterpret_cast<float*>(pgp + g.off_vrow)[tok_pos(lane)] = 0.f;
           }
           __syncwarp();
 #pragma unroll
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         }
         const uint32_t vidx4 = *reinterpret_cast<const uint32_t*>(pgp + g.off_vidx + gq * 4);
         float vrow[4] = {1.f, 1.f, 1.f, 1.f};
-        if (g.tx) {
+        if constexpr (TX) {
           const float4 vr = *reinterpret_cast<const float4*>(pgp + g.off_vrow + gq * 16);
           vrow[0] = vr.x; vrow[1] = vr.y; vrow[2] = vr.z; vrow[3] = vr.w;
         }
@@ -581,11 +581,11 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
             mrun[j][x] = m;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              p[x][u] = TH * j + HPT * tig + x < Gq ? ex2(sc[j][x][u] - base) : 0.f;
-              pv[x][u] = p[x][u] * vrow[u];
+              p[x][u] = ex2(sc[j][x][u] - base);  // (columns past the last head go along, unused)
+              pv[x][u] = TX ? p[x][u] * vrow[u] : p[x][u];
             }
             wfactor[x] = alpha[x];
-            if (g.tx) {
+            if constexpr (TX) {
               // p r has no bound of its own: the unit follows the largest so far, as far as that still counts
               float most = fmaxf(fmaxf(pv[x][0], pv[x][1]), fmaxf(pv[x][2], pv[x][3]));
               most = fmaxf(most, __shfl_xor_sync(kFull, most, 4));
@@ -626,12 +626,12 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
               zacc[j][x][2] = fmaf(pv[x][u], vz[u].z, zacc[j][x][2]);
               zacc[j][x][3] = fmaf(pv[x][u], vz[u].w, zacc[j][x][3]);
             }
-            if (g.tx) {
+            if constexpr (TX) {
               const float unit = exp2i(-vexp[j][x]);
 #pragma unroll
               for (int u = 0; u < 4; ++u) pv[x][u] *= unit;
             }
-            if (hh < Gq) {
+            {
 #pragma unroll
               for (int u = 0; u < 4; ++u)  // rounded to whole units by the addition of 1.5 * 2^23
                 atomicAdd(&Ww[hh * WR + vi[u]], __float_as_int(fmaf(pv[x][u], (float)(1 << kWBits), 12582912.0f)) - 0x4B400000);
@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 #pragma unroll
       for (int x = 0; x < HPT; ++x) {
         const int hh = TH * j + HPT * tig + x;
-        const float f0 = 16777216.0f / kVFac * exp2i(vexp[j][x]), f8 = f0 / Code<BITS>::kRow;
+        const float f0 = 16777216.0f / kVFac * (TX ? exp2i(vexp[j][x]) : 1.0f), f8 = f0 / Code<BITS>::kRow;
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
           mo[(warp * NH + hh) * kD + 16 * mt + gq] = (WIDE ? accv[j][mt][x] : accv[j][mt][0] + accv[j][mt][1]) * f0;
@@ -946,7 +946,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
   }
 }
 
-template <int BITS, int NT, bool WIDE>
+template <int BITS, int NT, bool WIDE, bool TX>
 cudaError_t launch_one(const Geom& g, const PagesArgs& a, cudaStream_t st) {
   const int smem = pages_smem((int)g.sub_bytes, NT, WIDE, g.P).total;
   // the kernel's shared-memory limit is raised when a call first needs more on this device
@@ -955,12 +955,12 @@ cudaError_t launch_one(const Geom& g, const PagesArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || allowed[dev].load(std::memory_order_relaxed) < smem) {
-    e = cudaFuncSetAttribute(decode_pages_kernel<BITS, NT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    e = cudaFuncSetAttribute(decode_pages_kernel<BITS, NT, WIDE, TX>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) allowed[dev].store(kMaxSmem, std::memory_order_relaxed);
   }
   if (!a.clustered) {
-    decode_pages_kernel<BITS, NT, WIDE><<<dim3(a.nsplit, g.H, g.B), kNW * 32, smem, st>>>(g, a);
+    decode_pages_kernel<BITS, NT, WIDE, TX><<<dim3(a.nsplit, g.H, g.B), kNW * 32, smem, st>>>(g, a);
     return cudaGetLastError();
   }
   cudaLaunchAttribute at{};
@@ -974,14 +974,14 @@ cudaError_t launch_one(const Geom& g, const PagesArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_pages_kernel<BITS, NT, WIDE>, g, a);
+  return cudaLaunchKernelEx(&cfg, decode_pages_kernel<BITS, NT, WIDE, TX>, g, a);
 }
 
-template <int BITS>
+template <int BITS, bool TX>
 cudaError_t launch_bits(const Geom& g, const PagesArgs& a, cudaStream_t st) {
-  if (a.Gq <= 4) return launch_one<BITS, 1, false>(g, a, st);
-  if (a.Gq <= 8) return launch_one<BITS, 1, true>(g, a, st);
-  return launch_one<BITS, 2, true>(g, a, st);
+  if (a.Gq <= 4) return launch_one<BITS, 1, false, TX>(g, a, st);
+  if (a.Gq <= 8) return launch_one<BITS, 1, true, TX>(g, a, st);
+  return launch_one<BITS, 2, true, TX>(g, a, st);
 }
 
 }  // namespace
@@ -1029,7 +1029,8 @@ cudaError_t launch_decode_pages(const Geom& g0, PagesArgs a, void* ws, cudaStrea
   a.arrivals = (int*)ws;
   a.part_ml = (float*)((uint8_t*)ws + counters_bytes(g));
   a.part_o = a.part_ml + 2 * (size_t)g.B * a.Hq * a.nsplit;
-  return g.bits == 2 ? launch_bits<2>(g, a, st) : launch_bits<4>(g, a, st);
+  if (g.tx) return g.bits == 2 ? launch_bits<2, true>(g, a, st) : launch_bits<4, true>(g, a, st);
+  return g.bits == 2 ? launch_bits<2, false>(g, a, st) : launch_bits<4, false>(g, a, st);
 }
 
 }  // namespace kvq
