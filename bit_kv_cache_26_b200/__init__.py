@@ -5,6 +5,11 @@ Argument marshalling only: every step of the computation runs in the CUDA kernel
 ``libkvq.so``.  PyTorch is used for device memory and streams.  There is no CPU or
 PyTorch fallback: importing this package fails if the library is missing.
 
+The calls around the cache's own (``kvq_plan_pages``, ``kvq_norm_rope``, ``kvq_page_bounds``,
+``kvq_select_pages``, ``kvq_decode_attention_pages``) make up the rest of a serving step at long
+context: page tables from request lengths, normed and rotated rows, and attention over the pages
+whose bounds promise the highest scores.
+
 Functions keep the C names (``kvq_mine_patterns``, ``kvq_quantize_append``,
 ``kvq_decode_attention``, ``kvq_dequantize`` ...); tensors are passed as torch CUDA
 tensors and the call is enqueued on the current torch stream unless ``stream`` is given.

@@ -2,10 +2,12 @@
 // of pages, softmax(q . K_hat^T) V_hat over their tokens only, in the cache's 2- or 4-bit codes
 // ("PatternKV", Section 3.4: the fused reconstruction and attention, over a subset of the pages).
 //
-// Bound: the listed sub-blocks from HBM.  One B200, 256 sequences x 8 KV heads x 128 of 512 pages in
-// 4 bits, 4 query heads each: 330 us, 4.9 TB/s of page bytes (0.75 of the copy bandwidth; the loop
-// alone streams at about 0.9, the rest is each CTA's setup and merge).  Before: pattern weights by
-// turn-taking in shared memory and both columns' products formed by both lanes, 481 us.
+// Bound: the listed sub-blocks from HBM, then instruction issue.  One B200, 256 sequences x 8 KV heads
+// x 128 of 512 pages in 4 bits, 4 query heads each: 326-336 us, 4.9 TB/s of page bytes (0.75 of the
+// copy bandwidth); 372 us back to back for a second, under the power cap at 1.72 GHz.  About 690 warp
+// instructions per page and head; the setup and merge of a CTA (lengths, ids, q . M_K, W . M_V) are an
+// eighth of its time.  The first form, with pattern weights added by lanes in turn and both lanes of
+// a head forming every product, took 481 us.
 //
 // Per CTA one (sequence, KV head, split of the list); each warp streams its entries' sub-blocks
 // through a ring of shared-memory stages (cp.async.bulk, bounded mbarrier waits).
