@@ -311,6 +311,7 @@ KVQ_API kvq_status kvq_decode_step(const kvq_cache* cache, const void* k_new, co
  * The rest of a serving step at long context, around the calls above:
  *   kvq_plan_pages -> kvq_norm_rope -> kvq_page_bounds -> kvq_quantize_append (or kvq_decode_step)
  *   -> kvq_select_pages -> kvq_decode_attention_pages.
+ * With a cache of no sequences (or no tokens to do) they write nothing.
  */
 
 /*

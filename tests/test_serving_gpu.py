@@ -100,6 +100,26 @@ def test_norm_rope_in_place_and_single_tensors(kvq):
     assert torch.equal(y, x)
 
 
+def test_norm_rope_in_place_on_slices_and_without_tokens(kvq):
+    g = gen(4)
+    wide = randn(g, 77, 9, D).to(torch.float16)
+    keep = wide.clone()
+    w = (1 + 0.3 * randn(g, D)).to(torch.float16)
+    pos = torch.arange(77, device="cuda", dtype=torch.int32)
+    inv = 10000.0 ** (-torch.arange(48, device="cuda", dtype=torch.float32) / 48)
+    q, k, v = wide[:, 1:6], wide[:, 6:8], wide[:, 8:]
+    kvq.kvq_norm_rope(q, k, v, pos, inv, q, k, v, w, None, 1e-6)
+    within(q, *rope_reference(keep[:, 1:6], w, pos, inv, 96, False, 1e-6))
+    within(k, *rope_reference(keep[:, 6:8], None, pos, inv, 96, False, 1e-6))
+    assert torch.equal(v, keep[:, 8:]) and torch.equal(wide[:, :1], keep[:, :1])
+    none = wide[:0]
+    kvq.kvq_norm_rope(none, None, none, pos[:0], inv, none, None, none)
+    one = wide[5:6].clone()                                          # one token: a stride nobody reads
+    out = torch.empty_like(one)
+    kvq.kvq_norm_rope(one.as_strided((1, 9, D), (1, D, 1)), None, None, pos[5:6], inv, out, None, None, w)
+    within(out, *rope_reference(one, w, pos[5:6], inv, 96, False, 1e-6))
+
+
 # ---- page plans ----------------------------------------------------------------------------------
 
 def plan_reference(L, n, table, free, count, most):
@@ -612,6 +632,86 @@ def test_a_captured_step_replays_on_new_inputs(kvq):
             within(eager.out, *attend_reference(kvq, eager.c, eager.q, eager.lists, eager.n, D ** -0.5))
     assert torch.equal(eager.bounds, replay.bounds)
     assert eager.c.read_status() == 0 and replay.c.read_status() == 0
+
+
+def test_a_serving_run_from_an_empty_table(kvq):
+    """Prompts, then steps of one token: plan -> rows -> bounds -> append -> selection -> attention, pages off one stack."""
+    B, H, Gq, prompt, steps, budget, maxp = 3, 2, 4, 70, 45, 3, 6
+    cache = kvq.PagedKVCache(B, H, maxp * G, 4, 8, page_order=torch.full((B * maxp,), -1, dtype=torch.int32), v_rho=0.3)
+    g = gen(21)
+    cache.k_patterns.normal_(generator=g)
+    cache.v_patterns.normal_(generator=g)
+    free = torch.randperm(cache.num_pages, generator=g, device="cuda").to(torch.int32)
+    count = torch.tensor([cache.num_pages], dtype=torch.int32, device="cuda")
+    bounds, plan_ws, sel_ws = cache.bounds(), cache.plan_workspace(), cache.select_workspace()
+    att_ws = cache.decode_pages_workspace(H * Gq, budget)
+    lists, n = torch.zeros(B, H, budget, dtype=torch.int32, device="cuda"), torch.zeros(B, H, dtype=torch.int32, device="cuda")
+    inv = 10000.0 ** (-torch.arange(64, device="cuda", dtype=torch.float32) / 64)
+    w = (1 + 0.2 * randn(g, D)).to(torch.bfloat16)
+    out = torch.zeros(B, H * Gq, D, dtype=torch.bfloat16, device="cuda")
+    keys, length = [], 0
+    for new in [prompt] + [1] * steps:
+        T = B * new
+        i32 = lambda *s: torch.full(s, -1, dtype=torch.int32, device="cuda")   # noqa: E731
+        cu, pos, ids, slots = i32(B + 1), i32(T), i32(T), torch.full((T,), -1, dtype=torch.int64, device="cuda")
+        cache.plan(torch.full((B,), new, dtype=torch.int32, device="cuda"), free, count, cu, slots, pos, ids, plan_ws)
+        x = randn(g, T, H * Gq + 2 * H, D).to(torch.bfloat16)
+        z = lambda h: torch.empty(T, h, D, dtype=torch.bfloat16, device="cuda")   # noqa: E731
+        q, k, v = z(H * Gq), z(H), z(H)
+        kvq.kvq_norm_rope(x[:, :H * Gq], x[:, H * Gq:H * Gq + H], x[:, H * Gq + H:], pos, inv, q, k, v, w, w)
+        kb, vb = k.view(B, new, H, D), v.view(B, new, H, D)
+        cache.update_bounds(kb, bounds)
+        cache.append(kb, vb)
+        keys.append(kb)
+        length += new
+        at = torch.arange(T, device="cuda")
+        assert torch.equal(pos.long(), length - new + at % new) and torch.equal(ids.long(), at // new)
+        assert torch.equal(slots, cache.page_table[ids.long(), pos.long() // G].long() * G + pos.long() % G)
+        last = q.view(B, new, H * Gq, D)[:, -1].contiguous()
+        cache.select(last, bounds, lists, n, sel_ws, sink=1, recent=1)
+        cache.decode_pages(last, lists, n, out, att_ws)
+        if length in (70, 71, 96, 97, 115):
+            within(out, *attend_reference(kvq, cache, last, lists, n, D ** -0.5))
+            want, wn = select_reference(last.float().cpu().numpy(), bounds.float().cpu().numpy(), cache.page_table.cpu().numpy(),
+                                        cache.seq_len.cpu().numpy(), H, budget, 1, 1)
+            assert np.array_equal(lists.cpu().numpy(), want) and np.array_equal(n.cpu().numpy(), wn)
+    allk = torch.cat(keys, 1).float()
+    for b in range(B):
+        for p in range(-(-length // G)):
+            rows = allk[b, p * G:(p + 1) * G]
+            page = bounds[int(cache.page_table[b, p])].float()
+            assert torch.equal(page[:, 0], rows.amin(0)) and torch.equal(page[:, 1], rows.amax(0))
+    used = cache.page_table[cache.page_table >= 0]
+    assert used.unique().numel() == used.numel() == B * 4 and int(count) == cache.num_pages - used.numel()
+    assert cache.read_status() == 0 and cache.seq_len.tolist() == [length] * B
+
+
+def test_two_calls_at_once_on_two_streams(kvq):
+    cache = filled(kvq, 2, 2, 0, 4, 8, torch.bfloat16, lengths=[3000, 2000])
+    qs = [randn(gen(s), 2, 8, D).to(torch.bfloat16) for s in range(2)]
+    bounds = randn(gen(8), cache.num_pages, 2, 2, D).sort(2).values.to(torch.bfloat16)
+    work = [dict(lists=torch.zeros(2, 2, 40, dtype=torch.int32, device="cuda"), n=torch.zeros(2, 2, dtype=torch.int32, device="cuda"),
+                 out=torch.zeros(2, 8, D, dtype=torch.bfloat16, device="cuda"), sel=cache.select_workspace(),
+                 att=cache.decode_pages_workspace(8, 40), stream=torch.cuda.Stream()) for _ in range(2)]
+
+    def go(w, q, stream):
+        cache.select(q, bounds, w["lists"], w["n"], w["sel"], stream=stream)
+        cache.decode_pages(q, w["lists"], w["n"], w["out"], w["att"], stream=stream)
+
+    want = []
+    for w, q in zip(work, qs):
+        go(w, q, None)
+        want.append((w["lists"].clone(), w["out"].clone()))
+    for _ in range(20):
+        for w in work:
+            w["lists"].zero_()
+            w["out"].zero_()
+        torch.cuda.synchronize()
+        for w, q in zip(work, qs):
+            go(w, q, w["stream"])
+        torch.cuda.synchronize()
+        for w, (lists, out) in zip(work, want):
+            assert torch.equal(w["lists"], lists) and torch.equal(w["out"], out)
 
 
 @pytest.mark.parametrize("B", [3, 2100])
