@@ -1029,8 +1029,9 @@ cudaError_t launch_decode_pages(const Geom& g0, PagesArgs a, void* ws, cudaStrea
   // 16 splits measured the same either way
   a.clustered = a.nsplit == 2 || a.nsplit == 4 || a.nsplit == 8;
   a.arrivals = (int*)ws;
-  a.part_ml = (float*)((uint8_t*)ws + counters_bytes(g));
-  a.part_o = a.part_ml + 2 * (size_t)g.B * a.Hq * a.nsplit;
+  // the rows of 128 first: they are read 16 bytes at a time, which an odd number of (max, sum) pairs before them would not allow
+  a.part_o = (float*)((uint8_t*)ws + counters_bytes(g));
+  a.part_ml = a.part_o + kD * (size_t)g.B * a.Hq * a.nsplit;
   if (g.tx) return g.bits == 2 ? launch_bits<2, true>(g, a, st) : launch_bits<4, true>(g, a, st);
   return g.bits == 2 ? launch_bits<2, false>(g, a, st) : launch_bits<4, false>(g, a, st);
 }

@@ -479,6 +479,18 @@ def test_attention_over_pages(kvq, dtype, bits, tx, H, Gq, P, lengths, budget):
     assert cache.read_status() == 0
 
 
+def test_attention_with_an_odd_number_of_partial_rows(kvq):
+    # one query head of one sequence, a list long enough for splits through the workspace, of which there is an odd number
+    cache = filled(kvq, 1, 1, 0, 4, 16, torch.bfloat16, lengths=[9000])
+    q = randn(gen(2), 1, 1, D).to(torch.bfloat16)
+    splits = lambda n: (kvq.kvq_decode_pages_workspace_bytes(cache.c, 1, n) - 256) // (130 * 4)   # noqa: E731
+    odd = [n for n in range(17, 282) if splits(n) > 16 and splits(n) % 2]
+    assert odd
+    for budget in (odd[0], odd[len(odd) // 2], odd[-1]):
+        lists, n = random_lists(cache, budget, 1)
+        within(attend(cache, q, lists, n), *attend_reference(kvq, cache, q, lists, n, D ** -0.5))
+
+
 def test_attention_over_every_page_is_decode_attention(kvq):
     cache = filled(kvq, 3, 2, 0, 4, 16, torch.bfloat16, lengths=[900, 31, 256])
     q = randn(gen(5), 3, 8, D).to(torch.bfloat16)
