@@ -137,7 +137,8 @@ __device__ __forceinline__ unsigned long long widen(uint32_t u) {
 // value is spread over, each half of the lanes goes on with half of the values).
 template <bool BF16>
 __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int Gq, const uint16_t* __restrict__ bounds, int b,
-                            int h, int p0, int p1, int lo_page, uint32_t* keys, float* W, uint8_t* ring) {
+                            int h, int p0, int p1, int lo_page, uint32_t* keys, float* W, uint8_t* ring,
+                            float minus_zero) {
   static_assert(kSelAhead == 4 && kSelRounds == 2, "the exchanges and waits below are written for these");
   constexpr int kStep = 2 * kSelAhead * kSelWarps;  // pages of a round of the block
   const int lane = threadIdx.x & 31, c = lane & 15, sub = lane >> 4;
@@ -204,6 +205,9 @@ __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int G
     up[e] = pk(W[8 * c + 2 * e], W[8 * c + 2 * e + 1]);
     dn[e] = pk(W[kD + 8 * c + 2 * e], W[kD + 8 * c + 2 * e + 1]);
   }
+  // a product and a sum of pairs may be compiled into one fused operation, which rounds once; x y + (-0), with a -0 that the
+  // compiler does not see, is the rounded product and can't be
+  const unsigned long long mz2 = pk(minus_zero, minus_zero);
   auto round = [&](int p, int r) {
     asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the newest round
     float x[kSelAhead];
@@ -214,7 +218,7 @@ __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int G
       const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, u[4] = {hi.x, hi.y, hi.z, hi.w};
       unsigned long long t[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] = addp(mul2(up[e], widen<BF16>(u[e])), mul2(dn[e], widen<BF16>(l[e])));
+      for (int e = 0; e < 4; ++e) t[e] = addp(fma2(up[e], widen<BF16>(u[e]), mz2), fma2(dn[e], widen<BF16>(l[e]), mz2));
       float s0, s1;
       upk(addp(addp(t[0], t[2]), addp(t[1], t[3])), s0, s1);
       x[i] = __fadd_rn(s0, s1);
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(kSelThreads, 6) select_pages_kernel(Geom g, Se
   if (k > 0) {
     const int per = (m + a.nsplit - 1) / a.nsplit;
     const int p0 = min(hi, lo + split * per), p1 = min(hi, p0 + per);
-    if (p0 < p1) score_pages<BF16>(g, a.q, a.Gq, a.bounds, b, h, p0, p1, lo, keys, W, ring);
+    if (p0 < p1) score_pages<BF16>(g, a.q, a.Gq, a.bounds, b, h, p0, p1, lo, keys, W, ring, a.minus_zero);
   }
   if (a.nsplit > 1) {
     __threadfence();
@@ -436,6 +440,7 @@ size_t select_workspace(const Geom& g) {
 
 cudaError_t launch_select(const Geom& g, SelectArgs a, void* ws, int num_sms, cudaStream_t st) {
   const size_t groups = (size_t)g.B * g.H;
+  a.minus_zero = -0.0f;
   a.arrivals = (int*)ws;
   a.keys = (uint32_t*)((uint8_t*)ws + (groups * sizeof(int) + 255) / 256 * 256);
   // as many CTAs as six per SM, each with 32 pages (one round of its warps) or more

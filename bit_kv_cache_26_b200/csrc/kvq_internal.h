@@ -63,6 +63,7 @@ struct SelectArgs {
   int* arrivals;
   uint32_t* keys;
   int nsplit;
+  float minus_zero;
 };
 size_t select_workspace(const Geom& g);
 cudaError_t launch_select(const Geom& g, SelectArgs a, void* ws, int num_sms, cudaStream_t st);

@@ -332,6 +332,32 @@ def test_select_pages(kvq, dtype, H, Gq, L, budget, sink, recent):
     assert cache.read_status() == 0
 
 
+def near_ties(Gq, pages, dt):
+    """Queries and page bounds whose scores lie within a few units of the last place of each other: one channel, with a hi that
+    varies and the lo that brings u hi + n lo back to the same value as nearly as the type can."""
+    g = torch.Generator().manual_seed(Gq + pages)
+    q = torch.zeros(1, Gq, D)
+    q[0, :, 77] = torch.randn(Gq, generator=g) * 0.3 ** torch.arange(Gq)   # W+ and W- of many bits
+    q = q.to(dt)
+    u, n = q[0, :, 77].double().clamp(min=0).sum(), q[0, :, 77].double().clamp(max=0).sum()
+    hi = (1 + torch.rand(pages, generator=g)).to(dt)
+    lo = ((u * 1.5 - u * hi.double()) / n).to(dt)
+    bounds = torch.zeros(pages, 1, 2, D, dtype=dt)
+    bounds[:, 0, 0, 77], bounds[:, 0, 1, 77] = lo, hi
+    return q, bounds
+
+
+@pytest.mark.parametrize("Gq,pages,budget", [(5, 1200, 376), (16, 264, 117), (10, 4000, 840)])
+def test_select_rounds_every_product_on_its_own(kvq, Gq, pages, budget):
+    """(With one rounding of u hi + fl(n lo) each of these would choose other pages.)"""
+    dt = torch.float16
+    cache = key_cache(kvq, 1, 1, pages, dt, [pages * G])
+    q, bounds = near_ties(Gq, pages, dt)
+    placed = torch.empty_like(bounds)
+    placed[cache.page_table[0].long().cpu()] = bounds
+    check_select(kvq, cache, q.cuda(), placed.cuda(), budget, 0, 1)
+
+
 def test_select_with_infinities_and_nan(kvq):
     dt, g = torch.float16, gen(9)
     cache = key_cache(kvq, 1, 1, 40, dt, [40 * G])
