@@ -3,11 +3,12 @@
 // ("PatternKV", Section 3.4: the fused reconstruction and attention, over a subset of the pages).
 //
 // Bound: the listed sub-blocks from HBM, then instruction issue.  One B200, 256 sequences x 8 KV heads
-// x 128 of 512 pages in 4 bits, 4 query heads each: 326-336 us, 4.9 TB/s of page bytes (0.75 of the
-// copy bandwidth); 372 us back to back for a second, under the power cap at 1.72 GHz.  About 690 warp
-// instructions per page and head; the setup and merge of a CTA (lengths, ids, q . M_K, W . M_V) are an
-// eighth of its time.  The first form, with pattern weights added by lanes in turn and both lanes of
-// a head forming every product, took 481 us.
+// x 128 of 512 pages in 4 bits, 4 query heads each: 311-321 us, 5.1-5.2 TB/s of page bytes (0.78-0.80 of
+// the copy bandwidth).  The setup and merge of a CTA (lengths, ids, q . M_K, W . M_V) are a tenth of its
+// time, and most of it where lists are short: they avoid branches and loads that wait for each other (all
+// query rows at once, four heads' sums exchanged together, the final sum eight patterns at a time), which
+// took 330 us here and 56 us for 78 at 912 groups of 3 pages with 5 query heads and 106 patterns.  The first
+// form, with pattern weights added by lanes in turn and both lanes of a head forming every product, took 481 us.
 //
 // Per CTA one (sequence, KV head, split of the list); each warp streams its entries' sub-blocks
 // through a ring of shared-memory stages (cp.async.bulk, bounded mbarrier waits).
@@ -117,8 +118,13 @@ __device__ __forceinline__ void split2(unsigned long long v, uint32_t& hi, uint3
 // Smallest row stride >= n whose rows start `step` banks apart.
 __host__ __device__ constexpr int banked(int n, int step) { return n + ((step - n) % 32 + 32) % 32; }
 
+constexpr int kMergeRows = 8;  // pattern weights of the final sum at a time
+// Row stride (floats) of the warps' sums of p v: a quad's four heads start 8 banks apart.
+__host__ __device__ constexpr int merge_row(bool wide) { return kD + (wide ? 4 : 8); }
+
 struct PagesSmem {
   int bars, qk, qinv, T, W, pex, total;
+  int wc, fsh, sum_o, sum_ml;  // of the merge, floats
   int t_row, w_row;
 };
 __host__ __device__ inline PagesSmem pages_smem(int sub_bytes, int NT, bool wide, int P) {
@@ -126,9 +132,12 @@ __host__ __device__ inline PagesSmem pages_smem(int sub_bytes, int NT, bool wide
   const int NH = NT * (wide ? 8 : 4);
   s.t_row = banked(P, wide ? 4 : 8);
   s.w_row = banked(P + 1, wide ? 4 : 8);  // +1: tokens stored raw
-  // the ring; the merge at the end reuses its place
-  const int merge = (kNW * NH * kD + 3 * kNW * NH + kNW * NH * 4 + P * NH + NH * kNW + NH * kD + 2 * NH) * 4;
-  int o = max(kNW * kStages * sub_bytes, merge);
+  // the ring; the merge at the end reuses its place: per warp and head 128 sums of p v, max, sum and unit, four sums of p z
+  s.wc = kNW * NH * merge_row(wide) + 3 * kNW * NH + kNW * NH * 4;
+  s.fsh = s.wc + (P + kMergeRows - 1) / kMergeRows * kMergeRows * NH;
+  s.sum_o = s.fsh + NH * kNW;
+  s.sum_ml = s.sum_o + NH * kD;
+  int o = max(kNW * kStages * sub_bytes, (s.sum_ml + 2 * NH) * 4);
   o = (o + 15) & ~15;
   s.bars = o; o += kNW * kStages * 8;
   s.qinv = o; o += NH * 4;                    // inverse power of two of the query scale per head
@@ -262,18 +271,20 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 
   // a group's sums, when they are merged in shared memory: [NH][128] sum p v and [NH] (max, sum p), after the merge's places
   const bool in_smem = a.nsplit == 1 || a.clustered;
-  float* sum_o = reinterpret_cast<float*>(smem) + kNW * NH * kD + 3 * kNW * NH + kNW * NH * 4 + P * NH + NH * kNW;
-  float2* sum_ml = reinterpret_cast<float2*>(sum_o + NH * kD);
+  const bool direct = !TX && a.nsplit == 1;  // a thread's channel is final (without the transform back): no exchange
+  float* sum_o = reinterpret_cast<float*>(smem) + sp.sum_o;
+  float2* sum_ml = reinterpret_cast<float2*>(reinterpret_cast<float*>(smem) + sp.sum_ml);
 
   if (n_mine > 0) {
     // the first of the setup's loads go out before the page copies, which would keep them waiting: this warp's
-    // query row and this thread's quarters of two pattern rows (four lanes per row, 16 bytes in turn)
-    uint16_t q_raw[4];
-    auto load_q = [&](int hh) {
-      const uint16_t* src = a.q + ((int64_t)b * a.Hq + (int64_t)h * Gq + min(hh, Gq - 1)) * kD + lane;
+    // query rows and this thread's quarters of two pattern rows (four lanes per row, 16 bytes in turn)
+    uint16_t q_raw[NH / kNW][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) q_raw[k] = __ldg(src + 32 * k);
-    };
+    for (int r = 0; r < NH / kNW; ++r) {
+      const uint16_t* src = a.q + ((int64_t)b * a.Hq + (int64_t)h * Gq + min(warp + kNW * r, Gq - 1)) * kD + lane;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q_raw[r][k] = __ldg(src + 32 * k);
+    }
     const int quarter = threadIdx.x & 3;
     float4 m[2][8];
     auto load_patterns = [&](int j) {
@@ -284,7 +295,6 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         for (int c = 0; c < 8; ++c) m[r][c] = __ldg(row + 4 * c);
       }
     };
-    load_q(warp);
     load_patterns(threadIdx.x >> 2);
     // the physical page of this lane's entry, -1 where it names none; whether it is the newest incomplete page
     const int my_n = (n_mine - warp + kNW - 1) / kNW;
@@ -326,11 +336,12 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
     }
 
     // ---- queries, T, zeroed W (over the first copies)
-    for (int hh = warp; hh < NH; hh += kNW) {
-      float v[4], m = 0.f;
-      if (hh > warp) load_q(hh);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = hh < Gq ? bits_to_float(q_raw[k], g.dtype) : 0.f;
+    for (int r = 0; r < NH / kNW; ++r) {
+      const int hh = warp + kNW * r;
+      float v[4], m = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = hh < Gq ? bits_to_float(q_raw[r][k], g.dtype) : 0.f;
       if constexpr (TX) {
         fwht_warp(v, lane);
 #pragma unroll
@@ -356,28 +367,38 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
     for (int j0 = 0; j0 < Pe; j0 += 64) {
       const int j = j0 + (threadIdx.x >> 2);
       if (j0 > 0) load_patterns(j);
-#pragma unroll 4
-      for (int hh = 0; hh < NH; ++hh) {
-        const float4* qr = reinterpret_cast<const float4*>(qn + hh * kD) + quarter;
-        unsigned long long s[2][2] = {{0ull, 0ull}, {0ull, 0ull}};
+#pragma unroll 1
+      for (int h0 = 0; h0 < NH; h0 += 4) {
+        float y[4][2];  // of heads h0 .. h0 + 3, this lane's quarter
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float4 x = qr[4 * c];
+        for (int hh = 0; hh < 4; ++hh) {
+          const float4* qr = reinterpret_cast<const float4*>(qn + (h0 + hh) * kD) + quarter;
+          unsigned long long s[2][2] = {{0ull, 0ull}, {0ull, 0ull}};
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float4 x = qr[4 * c];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              s[r][0] = fma2(pk(x.x, x.y), pk(m[r][c].x, m[r][c].y), s[r][0]);
+              s[r][1] = fma2(pk(x.z, x.w), pk(m[r][c].z, m[r][c].w), s[r][1]);
+            }
+          }
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            s[r][0] = fma2(pk(x.x, x.y), pk(m[r][c].x, m[r][c].y), s[r][0]);
-            s[r][1] = fma2(pk(x.z, x.w), pk(m[r][c].z, m[r][c].w), s[r][1]);
+            float x0, x1, x2, x3;
+            upk(s[r][0], x0, x1);
+            upk(s[r][1], x2, x3);
+            y[hh][r] = (x0 + x1) + (x2 + x3);
           }
         }
+        // summed over the four lanes, of which each goes on with fewer heads: lane `quarter` ends with head h0 + quarter
+        const bool q2 = quarter & 2, q1 = quarter & 1;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float x0, x1, x2, x3;
-          upk(s[r][0], x0, x1);
-          upk(s[r][1], x2, x3);
-          float y = (x0 + x1) + (x2 + x3);
-          y += __shfl_xor_sync(kFull, y, 1);
-          y += __shfl_xor_sync(kFull, y, 2);
-          if (quarter == 0 && j + 32 * r < Pe) T[hh * TR + j + 32 * r] = y;
+          const float u = (q2 ? y[2][r] : y[0][r]) + __shfl_xor_sync(kFull, q2 ? y[0][r] : y[2][r], 2);
+          const float v = (q2 ? y[3][r] : y[1][r]) + __shfl_xor_sync(kFull, q2 ? y[1][r] : y[3][r], 2);
+          const float w = (q1 ? v : u) + __shfl_xor_sync(kFull, q1 ? u : v, 1);
+          if (j + 32 * r < Pe) T[(h0 + quarter) * TR + j + 32 * r] = w;
         }
       }
     }
@@ -526,34 +547,46 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
             if constexpr (TX) reinterpret_cast<float*>(pgp + g.off_vrow)[tok_pos(lane)] = 0.f;
           }
           __syncwarp();
+          float acc[NT][2][4];
+          const uint16_t* qr[NT];
+          bool has[NT];
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
             const int hq = TH * j + (WIDE ? gq : gq >> 1);
-            const bool has = hq < Gq && (WIDE || part == 0);
-            const uint16_t* qr = a.q + ((int64_t)b * a.Hq + (int64_t)h * Gq + min(hq, Gq - 1)) * kD + 2 * tig;
+            has[j] = hq < Gq && (WIDE || part == 0);
+            qr[j] = a.q + ((int64_t)b * a.Hq + (int64_t)h * Gq + min(hq, Gq - 1)) * kD + 2 * tig;
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-              const uint32_t b0 = has ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks) : 0u;
-              const uint32_t b1 = has ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8) : 0u;
+            for (int x = 0; x < 8; ++x) acc[j][x >> 2][x & 3] = 0.f;
+          }
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            uint32_t f[2][4];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              const uint16_t* kr = kt + (16 * mt + gq) * kD + 16 * ks + 2 * tig;
+              f[mt][0] = *reinterpret_cast<const uint32_t*>(kr);
+              f[mt][1] = *reinterpret_cast<const uint32_t*>(kr + 8 * kD);
+              f[mt][2] = *reinterpret_cast<const uint32_t*>(kr + 8);
+              f[mt][3] = *reinterpret_cast<const uint32_t*>(kr + 8 * kD + 8);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const uint32_t b0 = has[j] ? *reinterpret_cast<const uint32_t*>(qr[j] + 16 * ks) : 0u;
+              const uint32_t b1 = has[j] ? *reinterpret_cast<const uint32_t*>(qr[j] + 16 * ks + 8) : 0u;
 #pragma unroll
               for (int mt = 0; mt < 2; ++mt) {
-                const uint16_t* kr = kt + (16 * mt + gq) * kD + 16 * ks + 2 * tig;
-                uint32_t f[4];
-                f[0] = *reinterpret_cast<const uint32_t*>(kr);
-                f[1] = *reinterpret_cast<const uint32_t*>(kr + 8 * kD);
-                f[2] = *reinterpret_cast<const uint32_t*>(kr + 8);
-                f[3] = *reinterpret_cast<const uint32_t*>(kr + 8 * kD + 8);
-                if (g.dtype == KVQ_BF16) mma_bf16(acc[mt], f, b0, b1);
-                else mma_f16(acc[mt], f, b0, b1);
+                if (g.dtype == KVQ_BF16) mma_bf16(acc[j][mt], f[mt], b0, b1);
+                else mma_f16(acc[j][mt], f[mt], b0, b1);
               }
             }
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int x = 0; x < HPT; ++x)
 #pragma unroll
               for (int u = 0; u < 4; ++u)
-                sc[j][x][u] = gq + 8 * u < ntail ? acc[u >> 1][2 * (u & 1) + x] * a.scale_log2 : -INFINITY;
-          }
+                sc[j][x][u] = gq + 8 * u < ntail ? acc[j][u >> 1][2 * (u & 1) + x] * a.scale_log2 : -INFINITY;
         }
         const uint32_t vidx4 = *reinterpret_cast<const uint32_t*>(pgp + g.off_vidx + gq * 4);
         float vrow[4] = {1.f, 1.f, 1.f, 1.f};
@@ -765,13 +798,14 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
           for (int u = 0; u < 4; ++u) zacc[j][x][u] += __shfl_xor_sync(kFull, zacc[j][x][u], o);
         }
     __syncthreads();  // every warp is done with its ring
-    float* mo = reinterpret_cast<float*>(smem);  // [kNW][NH][128]
-    float* mm = mo + kNW * NH * kD;              // [kNW][NH] max
+    constexpr int MO = merge_row(WIDE);
+    float* mo = reinterpret_cast<float*>(smem);  // [kNW][NH][MO]
+    float* mm = mo + kNW * NH * MO;              // [kNW][NH] max
     float* ml = mm + kNW * NH;                   // [kNW][NH] sum
     float* mz = ml + kNW * NH;                   // [kNW][NH][4]
     float* munit = mz + kNW * NH * 4;            // [kNW][NH] unit of the pattern weights
-    float* wc = munit + kNW * NH;                // [P][NH] merged pattern weights
-    float* fsh = wc + P * NH;                    // [NH][kNW] warp weights
+    float* wc = mo + sp.wc;                      // [P, to whole kMergeRows][NH] merged pattern weights
+    float* fsh = mo + sp.fsh;                    // [NH][kNW] warp weights
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -780,8 +814,8 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         const float f0 = 16777216.0f / kVFac * (TX ? exp2i(vexp[j][x]) : 1.0f), f8 = f0 / Code<BITS>::kRow;
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
-          mo[(warp * NH + hh) * kD + 16 * mt + gq] = (WIDE ? accv[j][mt][x] : accv[j][mt][0] + accv[j][mt][1]) * f0;
-          mo[(warp * NH + hh) * kD + 16 * mt + gq + 8] = (WIDE ? accv[j][mt][2 + x] : accv[j][mt][2] + accv[j][mt][3]) * f8;
+          mo[(warp * NH + hh) * MO + 16 * mt + gq] = (WIDE ? accv[j][mt][x] : accv[j][mt][0] + accv[j][mt][1]) * f0;
+          mo[(warp * NH + hh) * MO + 16 * mt + gq + 8] = (WIDE ? accv[j][mt][2 + x] : accv[j][mt][2] + accv[j][mt][3]) * f8;
         }
         if (gq == 0) {
           mm[warp * NH + hh] = mrun[j][x];
@@ -797,7 +831,9 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 #pragma unroll
     for (int j = 0; j < kMvAhead; ++j) mval[j] = __ldg(mv + (size_t)min(j, Pe - 1) * kD);
     __syncthreads();
-    for (int hh = warp; hh < Gq; hh += kNW) {
+    {
+      // the threads of a head are NH apart; each makes the weights of the warps for itself
+      const int hh = threadIdx.x % NH;
       float M = -INFINITY, Ls = 0.f, f[kNW];
 #pragma unroll
       for (int w = 0; w < kNW; ++w) M = fmaxf(M, mm[w * NH + hh]);
@@ -805,17 +841,22 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
       for (int w = 0; w < kNW; ++w) {
         f[w] = mm[w * NH + hh] == -INFINITY ? 0.f : ex2(mm[w * NH + hh] - M);
         Ls += f[w] * ml[w * NH + hh];
-        if (lane == w) fsh[hh * kNW + w] = f[w];
       }
-      if (lane == 0) {
-        if (in_smem) sum_ml[hh] = make_float2(M, Ls);
-        else reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(M, Ls);
+      if (threadIdx.x < NH) {
+        *reinterpret_cast<float4*>(fsh + hh * kNW) = make_float4(f[0], f[1], f[2], f[3]);
+        if (direct) sum_ml[hh].x = M > -INFINITY ? 1.0f / Ls : 1.0f;
+        else if (in_smem) sum_ml[hh] = make_float2(M, Ls);
+        else if (hh < Gq) reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(M, Ls);
       }
-      for (int jj = lane; jj < Pe; jj += 32) {
+#pragma unroll
+      for (int w = 0; w < kNW; ++w) f[w] *= munit[w * NH + hh];
+      const int rows = (Pe + kMergeRows - 1) / kMergeRows * kMergeRows;
+#pragma unroll 4
+      for (int jj = threadIdx.x / NH; jj < rows; jj += kNW * 32 / NH) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kNW; ++w) s = fmaf(f[w] * munit[w * NH + hh], (float)Wall[(w * NH + hh) * WR + jj], s);
-        wc[jj * NH + hh] = s;
+        for (int w = 0; w < kNW; ++w) s = fmaf(f[w], (float)Wall[(w * NH + hh) * WR + min(jj, Pe - 1)], s);
+        wc[jj * NH + hh] = jj < Pe ? s : 0.f;
       }
     }
     __syncthreads();
@@ -831,10 +872,12 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
           for (int j = 0; j < kMvAhead; ++j) mval[j] = __ldg(mv + (size_t)min(j0 + j, Pe - 1) * kD);
         }
 #pragma unroll
-        for (int j = 0; j < kMvAhead; ++j) {
-          if (j0 + j < Pe) {
-            const ulonglong2* w = reinterpret_cast<const ulonglong2*>(wc + (j0 + j) * NH);
-            const unsigned long long m2 = pk(mval[j], mval[j]);
+        for (int j = 0; j < kMvAhead; j += kMergeRows) {
+          if (j0 + j >= Pe) break;
+#pragma unroll
+          for (int e = 0; e < kMergeRows; ++e) {  // (rows past the last one have the weight 0)
+            const ulonglong2* w = reinterpret_cast<const ulonglong2*>(wc + (j0 + j + e) * NH);
+            const unsigned long long m2 = pk(mval[j + e], mval[j + e]);
 #pragma unroll
             for (int i = 0; i < NH / 4; ++i) {
               const ulonglong2 x = w[i];
@@ -848,13 +891,32 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 #pragma unroll
       for (int i = 0; i < NH / 2; ++i) upk(o2[i], o[2 * i], o[2 * i + 1]);
 #pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        if (i >= Gq) break;
+      for (int i = 0; i < NH; ++i) {  // (heads past the last one go along, unused)
+        const float4 f = *reinterpret_cast<const float4*>(fsh + i * kNW);
+        const float fw[kNW] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-        for (int w = 0; w < kNW; ++w)
-          o[i] = fmaf(fsh[i * kNW + w], mo[(w * NH + i) * kD + c] + mz[(w * NH + i) * 4 + (c >> 5)], o[i]);
-        if (in_smem) sum_o[i * kD + c] = o[i];
-        else a.part_o[(row0 + (int64_t)i * a.nsplit) * kD + c] = o[i];
+        for (int w = 0; w < kNW; ++w) o[i] = fmaf(fw[w], mo[(w * NH + i) * MO + c] + mz[(w * NH + i) * 4 + (c >> 5)], o[i]);
+      }
+      if (direct) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          if (i < Gq) {
+            const float v = o[i] * sum_ml[i].x;
+            bad = bad || !isfinite(v);
+            a.out[((int64_t)b * a.Hq + (int64_t)h * Gq + i) * kD + c] =
+                g.dtype == KVQ_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+          }
+        }
+        if (bad) set_status(g.status, KVQ_DEV_RANGE);
+        return;
+      }
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+        if (i < Gq) {
+          if (in_smem) sum_o[i * kD + c] = o[i];
+          else a.part_o[(row0 + (int64_t)i * a.nsplit) * kD + c] = o[i];
+        }
       }
     }
   } else {
@@ -869,29 +931,23 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
   if (in_smem) {
     if (a.nsplit > 1) cluster_sync(); else __syncthreads();
     for (int hh = split + a.nsplit * warp; hh < Gq; hh += a.nsplit * kNW) {
+      const float* row = sum_o + hh * kD + 4 * lane;
       float2 x = make_float2(-INFINITY, 0.f);
       if (lane < a.nsplit) x = a.nsplit > 1 ? peer_f2(sum_ml + hh, lane) : sum_ml[hh];
+      float4 y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = a.nsplit > 1 ? peer_f4(row, min(i, a.nsplit - 1)) : *reinterpret_cast<const float4*>(row);
       const float M = warp_max(x.x);
-      float Ls = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-      if (M > -INFINITY) {
-        const float fs = x.x == -INFINITY ? 0.f : ex2(x.x - M);
-        Ls = warp_sum(fs * x.y);
-        const float* row = sum_o + hh * kD + 4 * lane;
-        for (int i0 = 0; i0 < a.nsplit; i0 += 8) {
-          float4 y[8];
+      const float fs = x.x == -INFINITY ? 0.f : ex2(x.x - M), Ls = warp_sum(fs * x.y);
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            y[i] = a.nsplit > 1 ? peer_f4(row, min(i0 + i, a.nsplit - 1)) : *reinterpret_cast<const float4*>(row);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            // (a split without entries has written no row: its weight is 0, whatever is read; so past the last one)
-            const float f = __shfl_sync(kFull, fs, i0 + i);
-            o[0] += f == 0.f ? 0.f : f * y[i].x;
-            o[1] += f == 0.f ? 0.f : f * y[i].y;
-            o[2] += f == 0.f ? 0.f : f * y[i].z;
-            o[3] += f == 0.f ? 0.f : f * y[i].w;
-          }
-        }
+      for (int i = 0; i < 8; ++i) {
+        // (a split without entries has written no row: its weight is 0, whatever is read; so past the last one)
+        const float f = __shfl_sync(kFull, fs, i);
+        o[0] += f == 0.f ? 0.f : f * y[i].x;
+        o[1] += f == 0.f ? 0.f : f * y[i].y;
+        o[2] += f == 0.f ? 0.f : f * y[i].z;
+        o[3] += f == 0.f ? 0.f : f * y[i].w;
       }
       finish_head(g, o, M > -INFINITY ? Ls : 1.f, g.vcol + sh * kD, a.out + ((int64_t)b * a.Hq + (int64_t)h * Gq + hh) * kD, lane);
     }
