@@ -16,8 +16,9 @@
 //   the 16 sums halved (8, 4, 2, 1).  Equal scores: the lower page.  NaN ranks above all.
 //
 // Bound: HBM.  One B200: bounds of 8 x 32768 keys x 8 heads 94 us (6.1 TB/s, 0.93 of the copy
-// bandwidth); selection over 256 sequences x 8 heads x 512 pages 99 us (5.4 TB/s, 0.83), for one
-// sequence of 1024 pages 11 us of latency (lengths, page ids, bounds, the last CTA's choice).
+// bandwidth); selection over 256 sequences x 8 heads x 512 pages 100 us (5.4 TB/s, 0.82), for one
+// sequence of 1024 pages 10.5 us of latency (lengths, page ids, bounds, the last CTA's choice).  The
+// query heads are loaded before the first is used: 16 heads a group in turn took 12.8 us for 9.2 there.
 #include <algorithm>
 #include <atomic>
 
@@ -183,9 +184,12 @@ __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int G
   static_assert(kSelThreads == kD, "a thread per channel of W+ and W-");
   {
     float v[16];
+    uint16_t raw[16];  // all loads before the first use
+    const uint16_t* src = q + ((int64_t)b * g.H * Gq + (int64_t)h * Gq) * kD + threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      v[i] = i < Gq ? load_elem(q + ((int64_t)b * g.H * Gq + (int64_t)h * Gq + i) * kD + threadIdx.x, g.dtype) : 0.f;
+    for (int i = 0; i < 16; ++i) raw[i] = __ldg(src + min(i, Gq - 1) * kD);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i < Gq ? bits_to_float(raw[i], BF16 ? KVQ_BF16 : KVQ_F16) : 0.f;
 #pragma unroll
     for (int neg = 0; neg < 2; ++neg) {
       float w[16];
