@@ -1047,9 +1047,11 @@ cudaError_t launch_bits(const Geom& g, const PagesArgs& a, cudaStream_t st) {
 // Splits of the list: 1, 2, 4 or 8 (a cluster, whose sums meet in shared memory), or 16 and more (through the workspace).
 // Model, in units of the time a lone CTA takes for a page per warp (1.3 us on one B200): k CTAs on an SM at once take
 // max(1, 0.48 k) for a page per warp and 5 + 1.25 (k - 1) before and after the loop; the busiest SM runs its CTAs `occ` at a
-// time; merging costs a little per split.  At most kWarpEntries entries per warp.  Measured (through the workspace) at 64
-// listed pages of 4 bits for 8 groups (best 16 splits, 12.7 us; 1: 29 us; 64: 23 us), for 64 groups (best 4), at 256 pages
-// for 8 groups (best 16), at 128 pages for 256 groups (best 2) and 2048 (1).  These are the model's choices.
+// time; merging costs a little per split, and more per head through the workspace (8 groups of 64 pages, 8 splits and 16:
+// 11.3 and 11.2 us with 4 heads a group, 13.8 and 14.8 with 8, 18.4 and 22.0 with 16).  At most kWarpEntries entries per
+// warp.  Measured with 4, 8 and 16 heads a group at 64 listed pages for 8 groups (best 8 splits; 1: 27, 39 and 60 us; 64:
+// 18, 35 and 53), 128 groups (2) and 1024 (1), at 256 pages for 16 (16), at 128 pages for 256 (1; with 4 heads 2 are a
+// twentieth faster), at 452 pages for 3 (33): the model's choice or within a tenth of it.
 int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms) {
   const int64_t units = std::max<int64_t>(1, (int64_t)g.B * g.H), sms = std::max(1, num_sms);
   const bool wide = Gq > 4;
@@ -1065,7 +1067,7 @@ int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms) {
     if (ns < least) continue;
     const int64_t per_sm = (units * ns + sms - 1) / sms, full = per_sm / occ, rem = per_sm % occ;
     const int pages = ((budget + ns - 1) / ns + kNW - 1) / kNW;
-    const double cost = full * round(occ, pages) + (rem ? round(rem, pages) : 0.0) + 0.05 * ns;
+    const double cost = full * round(occ, pages) + (rem ? round(rem, pages) : 0.0) + 0.05 * ns + (ns >= 16 ? 0.2 * Gq : 0.0);
     if (cost < best_cost * (1.0 - 1e-9)) { best_cost = cost; best = ns; }
   }
   return best;
