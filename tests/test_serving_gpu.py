@@ -83,6 +83,25 @@ def test_norm_rope(kvq, dtype, tokens, hq, hk, rot, inter, norm):
     assert (qo[:, hq] == 7.0).all()                                 # rows beside the output stay
 
 
+@pytest.mark.parametrize("tokens,heads,weights,rot,inter", [
+    (37, (8, 1, 1), "qk", 128, False), (37, (3, 1, 2), "k", 96, True), (1, (1, 1, 1), "q", 64, False), (20011, (1, 1, 1), "qk", 32, True),
+    (37, (2, 3, 6), "", 128, False), (9001, (0, 2, 1), "k", 128, True), (513, (6, 0, 1), "q", 112, False),
+])
+def test_norm_rope_of_few_heads(kvq, tokens, heads, weights, rot, inter):
+    dt, g = torch.bfloat16, gen(sum(heads) + rot)
+    rows = [randn(g, tokens, n, D).to(dt) if n else None for n in heads]
+    rows[2][0, 0, :4] = torch.tensor([float("nan"), float("inf"), -0.0, 0.0], device="cuda", dtype=dt)   # values pass as they are
+    w = [(1 + 0.3 * randn(g, D)).to(dt) if n in weights else None for n in "qk"]
+    pos = torch.randint(0, 1 << 20, (tokens,), generator=g, device="cuda", dtype=torch.int32)
+    inv = 10000.0 ** (-torch.arange(rot // 2, device="cuda", dtype=torch.float32) / (rot // 2))
+    out = [None if x is None else torch.full_like(x, 7.0) for x in rows]
+    kvq.kvq_norm_rope(*rows, pos, inv, *out, *w, 1e-6, inter)
+    for x, y, z in zip(rows[:2], out[:2], w):
+        if x is not None:
+            within(y, *rope_reference(x, z, pos, inv, rot, inter, 1e-6))
+    assert torch.equal(out[2].view(torch.int16), rows[2].view(torch.int16))
+
+
 def test_norm_rope_in_place_and_single_tensors(kvq):
     g = gen(3)
     x = randn(g, 45, 6, D).to(torch.bfloat16)
