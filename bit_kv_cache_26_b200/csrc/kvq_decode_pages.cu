@@ -103,16 +103,30 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
   return h;
 }
-// fp16 pairs of the hi parts (11 significant bits) of two fp32 values and of what is left of them.
-__device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-  hi = half2_of(v0, v1);
-  const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  lo = half2_of(v0 - t.x, v1 - t.y);
+__device__ __forceinline__ unsigned long long less(unsigned long long v, float x, float y) {  // v - (x, y)
+  return fma2(pk(x, y), pk(-1.0f, -1.0f), v);
 }
+// fp16 pairs of the hi parts (11 significant bits) of two fp32 values and of what is left of them.
 __device__ __forceinline__ void split2(unsigned long long v, uint32_t& hi, uint32_t& lo) {
   float v0, v1;
   upk(v, v0, v1);
-  split2(v0, v1, hi, lo);
+  hi = half2_of(v0, v1);
+  const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  upk(less(v, t.x, t.y), v0, v1);
+  lo = half2_of(v0, v1);
+}
+// The same of the pairs (first of v, first of w) and (second of v, second of w).
+__device__ __forceinline__ void split2x2(unsigned long long v, unsigned long long w, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+  float v0, v1, w0, w1;
+  upk(v, v0, v1);
+  upk(w, w0, w1);
+  hi[0] = half2_of(v0, w0);
+  hi[1] = half2_of(v1, w1);
+  const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&hi[0])), t = __half22float2(*reinterpret_cast<const __half2*>(&hi[1]));
+  upk(less(v, s.x, t.x), v0, v1);
+  upk(less(w, s.y, t.y), w0, w1);
+  lo[0] = half2_of(v0, w0);
+  lo[1] = half2_of(v1, w1);
 }
 
 // Smallest row stride >= n whose rows start `step` banks apart.
@@ -704,20 +718,15 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
           const unsigned long long q0 = pk(p0[0], p0[0]), q1 = pk(p0[1], p0[1]), q2 = pk(p0[2], p0[2]), q3 = pk(p0[3], p0[3]);
 #pragma unroll
           for (int gp = 0; gp < 2; ++gp) {  // two channel groups at a time: their scales are neighbours
-            float v0[2], v1[2], v2[2], v3[2];
-            upk(mul2(q0, gp ? pk(s0.z, s0.w) : pk(s0.x, s0.y)), v0[0], v0[1]);
-            upk(mul2(q1, gp ? pk(s1.z, s1.w) : pk(s1.x, s1.y)), v1[0], v1[1]);
-            upk(mul2(q2, gp ? pk(s2.z, s2.w) : pk(s2.x, s2.y)), v2[0], v2[1]);
-            upk(mul2(q3, gp ? pk(s3.z, s3.w) : pk(s3.x, s3.y)), v3[0], v3[1]);
+            uint32_t own0[2], own1[2], lo0[2], lo1[2];
+            split2x2(mul2(q0, gp ? pk(s0.z, s0.w) : pk(s0.x, s0.y)), mul2(q1, gp ? pk(s1.z, s1.w) : pk(s1.x, s1.y)), own0, lo0);
+            split2x2(mul2(q2, gp ? pk(s2.z, s2.w) : pk(s2.x, s2.y)), mul2(q3, gp ? pk(s3.z, s3.w) : pk(s3.x, s3.y)), own1, lo1);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              uint32_t own0, own1, lo0, lo1;
-              split2(v0[x], v1[x], own0, lo0);
-              split2(v2[x], v3[x], own1, lo1);
-              const uint32_t got0 = __shfl_xor_sync(kFull, lo0, 4), got1 = __shfl_xor_sync(kFull, lo1, 4);
+              const uint32_t got0 = __shfl_xor_sync(kFull, lo0[x], 4), got1 = __shfl_xor_sync(kFull, lo1[x], 4);
 #pragma unroll
               for (int ks = 0; ks < 2; ++ks) {
-                const uint32_t b0 = part == ks ? own0 : got0, b1 = part == ks ? own1 : got1;
+                const uint32_t b0 = part == ks ? own0[x] : got0, b1 = part == ks ? own1[x] : got1;
 #pragma unroll
                 for (int mh = 0; mh < 2; ++mh) {
                   const int mt = (2 * gp + x) * 2 + mh;
@@ -741,23 +750,18 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
               const unsigned long long q0 = pk(pa.x, pa.x), q1 = pk(pb.x, pb.x), q2 = pk(pa.y, pa.y), q3 = pk(pb.y, pb.y);
 #pragma unroll
               for (int gp = 0; gp < 2; ++gp) {
-                float v0[2], v1[2], v2[2], v3[2];
-                upk(mul2(q0, gp ? pk(s0.z, s0.w) : pk(s0.x, s0.y)), v0[0], v0[1]);
-                upk(mul2(q1, gp ? pk(s1.z, s1.w) : pk(s1.x, s1.y)), v1[0], v1[1]);
-                upk(mul2(q2, gp ? pk(s2.z, s2.w) : pk(s2.x, s2.y)), v2[0], v2[1]);
-                upk(mul2(q3, gp ? pk(s3.z, s3.w) : pk(s3.x, s3.y)), v3[0], v3[1]);
+                uint32_t bh0[2], bh1[2], bl0[2], bl1[2];
+                split2x2(mul2(q0, gp ? pk(s0.z, s0.w) : pk(s0.x, s0.y)), mul2(q1, gp ? pk(s1.z, s1.w) : pk(s1.x, s1.y)), bh0, bl0);
+                split2x2(mul2(q2, gp ? pk(s2.z, s2.w) : pk(s2.x, s2.y)), mul2(q3, gp ? pk(s3.z, s3.w) : pk(s3.x, s3.y)), bh1, bl1);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  uint32_t bh0, bh1, bl0, bl1;
-                  split2(v0[x], v1[x], bh0, bl0);
-                  split2(v2[x], v3[x], bh1, bl1);
 #pragma unroll
                   for (int mh = 0; mh < 2; ++mh) {
                     const int mt = (2 * gp + x) * 2 + mh;
                     uint32_t f[4];
                     frag16<BITS>(BITS == 2 ? vw[mt] : vw[mt * 2 + ks], ks, f);
-                    mma_f16(accv[j][mt], f, bh0, bh1);
-                    mma_f16(accv[j][mt], f, bl0, bl1);
+                    mma_f16(accv[j][mt], f, bh0[x], bh1[x]);
+                    mma_f16(accv[j][mt], f, bl0[x], bl1[x]);
                   }
                 }
               }
