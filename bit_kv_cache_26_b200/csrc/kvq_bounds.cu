@@ -120,11 +120,6 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-__device__ __forceinline__ unsigned long long addp(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 template <bool BF16>
 __device__ __forceinline__ unsigned long long widen(uint32_t u) {
   if constexpr (BF16) return pk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
@@ -222,9 +217,9 @@ __device__ void score_pages(const Geom& g, const uint16_t* __restrict__ q, int G
       const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, u[4] = {hi.x, hi.y, hi.z, hi.w};
       unsigned long long t[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] = addp(fma2(up[e], widen<BF16>(u[e]), mz2), fma2(dn[e], widen<BF16>(l[e]), mz2));
+      for (int e = 0; e < 4; ++e) t[e] = add2(fma2(up[e], widen<BF16>(u[e]), mz2), fma2(dn[e], widen<BF16>(l[e]), mz2));
       float s0, s1;
-      upk(addp(addp(t[0], t[2]), addp(t[1], t[3])), s0, s1);
+      upk(add2(add2(t[0], t[2]), add2(t[1], t[3])), s0, s1);
       x[i] = __fadd_rn(s0, s1);
     }
     const unsigned none = gone[r];

@@ -539,12 +539,14 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 #pragma unroll
             for (int x = 0; x < HPT; ++x) {
               const float z = __shfl_sync(kFull, zk[j], WIDE ? 4 * (2 * tig + x) : 8 * tig);
-              constexpr float f0 = 16777216.0f, f8 = 16777216.0f / Code<BITS>::kRow;
+              const unsigned long long f08 = pk(16777216.0f, 16777216.0f / Code<BITS>::kRow), z2 = pk(z, z), l2 = pk(scl[j][x], scl[j][x]);
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const float s = WIDE ? acc[j][u >> 1][2 * (u & 1) + x] : acc[j][u >> 1][2 * (u & 1)] + acc[j][u >> 1][2 * (u & 1) + 1];
-                const int idx = min((int)((kidx4 >> (8 * u)) & 0xff), Pe - 1);
-                sc[j][x][u] = (fmaf(s, u & 1 ? f8 : f0, z) + T[(TH * j + HPT * tig + x) * TR + idx]) * (TX ? krow[u] * scl[j][x] : scl[j][x]);
+              for (int hf = 0; hf < 2; ++hf) {  // tokens gq + 16 hf and the one 8 on
+                const float s0 = WIDE ? acc[j][hf][x] : acc[j][hf][0] + acc[j][hf][1], s8 = WIDE ? acc[j][hf][2 + x] : acc[j][hf][2] + acc[j][hf][3];
+                const int i0 = min((int)((kidx4 >> (16 * hf)) & 0xff), Pe - 1), i8 = min((int)((kidx4 >> (16 * hf + 8)) & 0xff), Pe - 1);
+                const float* Th = T + (TH * j + HPT * tig + x) * TR;
+                const unsigned long long s = add2(fma2(pk(s0, s8), f08, z2), pk(Th[i0], Th[i8]));
+                upk(mul2(s, TX ? mul2(pk(krow[2 * hf], krow[2 * hf + 1]), l2) : l2), sc[j][x][2 * hf], sc[j][x][2 * hf + 1]);
               }
             }
           }
@@ -629,9 +631,13 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
             alpha[x] = ex2(mrun[j][x] - base);
             mrun[j][x] = m;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              p[x][u] = ex2(sc[j][x][u] - base);  // (columns past the last head go along, unused)
+            for (int u = 0; u < 4; u += 2) {
+              float d0, d1;
+              upk(add2(pk(sc[j][x][u], sc[j][x][u + 1]), pk(-base, -base)), d0, d1);
+              p[x][u] = ex2(d0);  // (columns past the last head go along, unused)
+              p[x][u + 1] = ex2(d1);
               pv[x][u] = TX ? p[x][u] * vrow[u] : p[x][u];
+              pv[x][u + 1] = TX ? p[x][u + 1] * vrow[u + 1] : p[x][u + 1];
             }
             wfactor[x] = alpha[x];
             if constexpr (TX) {
@@ -681,14 +687,22 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
               for (int u = 0; u < 4; ++u) pv[x][u] *= unit;
             }
             {
+              constexpr float kUnits = 1 << kWBits;
 #pragma unroll
-              for (int u = 0; u < 4; ++u)  // rounded to whole units by the addition of 1.5 * 2^23
-                atomicAdd(&Ww[hh * WR + vi[u]], __float_as_int(fmaf(pv[x][u], (float)(1 << kWBits), 12582912.0f)) - 0x4B400000);
+              for (int u = 0; u < 4; u += 2) {  // rounded to whole units by the addition of 1.5 * 2^23
+                float w0, w1;
+                upk(fma2(pk(pv[x][u], pv[x][u + 1]), pk(kUnits, kUnits), pk(12582912.0f, 12582912.0f)), w0, w1);
+                atomicAdd(&Ww[hh * WR + vi[u]], __float_as_int(w0) - 0x4B400000);
+                atomicAdd(&Ww[hh * WR + vi[u + 1]], __float_as_int(w1) - 0x4B400000);
+              }
             }
             // p to the lanes of the V columns, scaled; tokens 8..15 of each 16 are columns with a factor of their own
             constexpr float f0 = kVFac, f8 = kVFac / Code<BITS>::kCol;
             if constexpr (WIDE) {
-              *reinterpret_cast<float4*>(pex + hh * kPexRow + gq * 4) = make_float4(pv[x][0] * f0, pv[x][1] * f8, pv[x][2] * f0, pv[x][3] * f8);
+              float y[4];
+              upk(mul2(pk(pv[x][0], pv[x][1]), pk(f0, f8)), y[0], y[1]);
+              upk(mul2(pk(pv[x][2], pv[x][3]), pk(f0, f8)), y[2], y[3]);
+              *reinterpret_cast<float4*>(pex + hh * kPexRow + gq * 4) = make_float4(y[0], y[1], y[2], y[3]);
             } else {
               // Lane (head, part) wants tokens 2 tig and 2 tig + 1 (+ 8) of the page's half `part`: u = 2 part, 2 part + 1.
               // Even token rows offer the halves in one order, odd rows in the other, so that both exchanges serve both
