@@ -3,12 +3,15 @@
 // ("PatternKV", Section 3.4: the fused reconstruction and attention, over a subset of the pages).
 //
 // Bound: the listed sub-blocks from HBM, then instruction issue.  One B200, 256 sequences x 8 KV heads
-// x 128 of 512 pages in 4 bits, 4 query heads each: 311-321 us, 5.1-5.2 TB/s of page bytes (0.78-0.80 of
-// the copy bandwidth).  The setup and merge of a CTA (lengths, ids, q . M_K, W . M_V) are a tenth of its
-// time, and most of it where lists are short: they avoid branches and loads that wait for each other (all
-// query rows at once, four heads' sums exchanged together, the final sum eight patterns at a time), which
-// took 330 us here and 56 us for 78 at 912 groups of 3 pages with 5 query heads and 106 patterns.  The first
-// form, with pattern weights added by lanes in turn and both lanes of a head forming every product, took 481 us.
+// x 128 of 512 pages in 4 bits, 4 query heads each: 308-317 us, 5.2-5.3 TB/s of page bytes (0.78-0.81 of
+// the copy bandwidth); 361 us back to back, under the power cap.  With 8 and 16 heads a group (1024
+// groups of 64 pages) 135 and 264 us for 63 of bytes: the work per page grows with the heads, and 12 and
+// 8 warps an SM hide less of it.  The setup and merge of a CTA (lengths, ids, q . M_K, W . M_V) are a
+// tenth of the first and most of the time of short lists: they avoid branches and loads that wait for
+// each other (all query rows at once, four heads' sums exchanged together, the final sum eight patterns
+// at a time), which took 55 us for 78 at 912 groups of 3 pages with 5 query heads and 106 patterns.  The
+// first form, with pattern weights added by lanes in turn and both lanes of a head forming every
+// product, took 481 us in the first case; scalar instead of packed pairs in the loop 324.
 //
 // Per CTA one (sequence, KV head, split of the list); each warp streams its entries' sub-blocks
 // through a ring of shared-memory stages (cp.async.bulk, bounded mbarrier waits).
@@ -190,6 +193,10 @@ __device__ __forceinline__ float4 peer_f4(const void* p, int r) {
                : "memory");
   return v;
 }
+
+// What a head's sum of p v is divided by.  The sum of p is 1 or more with any token, and 0 with none, for which the output is
+// 0; a query of NaN has no maximum (it is ignored) and a sum of NaN, which is left to show in the output.
+__device__ __forceinline__ float sum_or_one(float l) { return l == 0.f ? 1.f : l; }
 
 // Output of one query head from its channels 4 lane .. 4 lane + 3 of sum p v and its sum p.
 __device__ __forceinline__ void finish_head(const Geom& g, float (&o)[4], float l, const float* vcol, uint16_t* out, int lane) {
@@ -862,7 +869,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
       }
       if (threadIdx.x < NH) {
         *reinterpret_cast<float4*>(fsh + hh * kNW) = make_float4(f[0], f[1], f[2], f[3]);
-        if (direct) sum_ml[hh].x = M > -INFINITY ? 1.0f / Ls : 1.0f;
+        if (direct) sum_ml[hh].x = 1.0f / sum_or_one(Ls);
         else if (in_smem) sum_ml[hh] = make_float2(M, Ls);
         else if (hh < Gq) reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(M, Ls);
       }
@@ -967,7 +974,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         o[2] += f == 0.f ? 0.f : f * y[i].z;
         o[3] += f == 0.f ? 0.f : f * y[i].w;
       }
-      finish_head(g, o, M > -INFINITY ? Ls : 1.f, g.vcol + sh * kD, a.out + ((int64_t)b * a.Hq + (int64_t)h * Gq + hh) * kD, lane);
+      finish_head(g, o, sum_or_one(Ls), g.vcol + sh * kD, a.out + ((int64_t)b * a.Hq + (int64_t)h * Gq + hh) * kD, lane);
     }
     if (a.nsplit > 1) cluster_sync();  // the others' reads of this CTA's sums are done
     return;
@@ -994,31 +1001,29 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
     for (int s = 32 + lane; s < a.nsplit; s += 32) M = fmaxf(M, __ldcg(ml + s).x);
     M = warp_max(M);
     float Ls = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    if (M > -INFINITY) {
-      for (int s0 = 0; s0 < a.nsplit; s0 += 32) {
-        if (s0 > 0) x = s0 + lane < a.nsplit ? __ldcg(ml + s0 + lane) : make_float2(-INFINITY, 0.f);
-        const float fs = x.x == -INFINITY ? 0.f : ex2(x.x - M);
-        Ls = fmaf(fs, x.y, Ls);
-        const int n = min(32, a.nsplit - s0);
-        for (int i0 = 0; i0 < n; i0 += 8) {
-          float4 y[8];
+    for (int s0 = 0; s0 < a.nsplit; s0 += 32) {
+      if (s0 > 0) x = s0 + lane < a.nsplit ? __ldcg(ml + s0 + lane) : make_float2(-INFINITY, 0.f);
+      const float fs = x.x == -INFINITY ? 0.f : ex2(x.x - M);
+      Ls = fmaf(fs, x.y, Ls);
+      const int n = min(32, a.nsplit - s0);
+      for (int i0 = 0; i0 < n; i0 += 8) {
+        float4 y[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            y[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (base + min(s0 + i0 + i, a.nsplit - 1)) * kD) + lane);
+        for (int i = 0; i < 8; ++i)
+          y[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (base + min(s0 + i0 + i, a.nsplit - 1)) * kD) + lane);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            // (a split without entries has written no row: its weight is 0, whatever is read; so past the last one)
-            const float f = __shfl_sync(kFull, fs, i0 + i);
-            o[0] += f == 0.f ? 0.f : f * y[i].x;
-            o[1] += f == 0.f ? 0.f : f * y[i].y;
-            o[2] += f == 0.f ? 0.f : f * y[i].z;
-            o[3] += f == 0.f ? 0.f : f * y[i].w;
-          }
+        for (int i = 0; i < 8; ++i) {
+          // (a split without entries has written no row: its weight is 0, whatever is read; so past the last one)
+          const float f = __shfl_sync(kFull, fs, i0 + i);
+          o[0] += f == 0.f ? 0.f : f * y[i].x;
+          o[1] += f == 0.f ? 0.f : f * y[i].y;
+          o[2] += f == 0.f ? 0.f : f * y[i].z;
+          o[3] += f == 0.f ? 0.f : f * y[i].w;
         }
       }
-      Ls = warp_sum(Ls);
     }
-    finish_head(g, o, M > -INFINITY ? Ls : 1.f, g.vcol + sh * kD, outp, lane);
+    Ls = warp_sum(Ls);
+    finish_head(g, o, sum_or_one(Ls), g.vcol + sh * kD, outp, lane);
   }
 }
 

@@ -599,6 +599,23 @@ def test_attention_without_entries_is_zero_and_bad_entries_are_passed_over(kvq):
     within(out, *attend_reference(kvq, cache, q, only, torch.tensor([[1], [2]], device="cuda"), D ** -0.5))
 
 
+@pytest.mark.parametrize("B,H,Gq,budget,tx", [(40, 8, 4, 3, 0), (1, 1, 4, 8, 0), (1, 2, 5, 60, 1), (1, 1, 16, 60, 0), (3, 1, 8, 61, 1)])
+def test_a_nan_in_a_query_shows_in_its_head_only(kvq, B, H, Gq, budget, tx):
+    """(One group and 60 pages: splits that meet in the workspace; 8: in a cluster; 320 groups: none.)"""
+    dt = torch.bfloat16
+    cache = filled(kvq, B, H, 61 * G if B < 40 else 3 * G + 5, 4, 8, dt, tx=tx)
+    q = randn(gen(5), B, H * Gq, D).to(dt)
+    lists, n = random_lists(cache, budget, 6)
+    assert n[0, 0] > 0
+    want = attend(cache, q, lists, n)
+    q[0, Gq // 2, 17] = float("nan")
+    got = attend(cache, q, lists, n)
+    assert torch.isnan(got[0, Gq // 2]).all()
+    got[0, Gq // 2] = want[0, Gq // 2]
+    # the others: the same sums up to an fp32 rounding of a rescaled weight (2^-24), so at most the neighbouring number
+    assert torch.allclose(got.float(), want.float(), rtol=torch.finfo(dt).eps, atol=1e-6)
+
+
 def test_attention_of_extreme_rows(kvq):
     # a zero query (every token weighs the same), one query head far above the others, and tiny values
     cache = filled(kvq, 1, 1, 0, 4, 4, torch.float16, lengths=[160])
