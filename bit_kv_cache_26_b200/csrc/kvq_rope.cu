@@ -165,6 +165,9 @@ cudaError_t launch_norm_rope(const RopeArgs& a0, int dtype, bool interleaved, in
   const int64_t groups = (a.rows[0].heads + 3) / 4 + (a.rows[1].heads + 3) / 4 + (a.rows[2].heads + 3) / 4;
   const int64_t warps = (int64_t)num_sms * 32;
   a.parts = (int)std::min(groups, std::max<int64_t>(1, warps / a.tokens));
+  // One to three waves of warps: halves even out the last one, where the angles made twice are little beside the rows (12
+  // groups a token, 5000, 10000 and 20000 tokens: 32, 51 and 90 us whole, 28, 49 and 90 in halves; 9 groups, 8191 tokens: 31, 33).
+  if (a.parts == 1 && groups >= 10 && a.tokens < 3 * warps) a.parts = 2;
   const int64_t grid = (a.tokens * a.parts + kRopeWarps - 1) / kRopeWarps;
   const bool bf = dtype == KVQ_BF16;
   auto* k = bf ? (interleaved ? norm_rope_kernel<true, true> : norm_rope_kernel<true, false>)
