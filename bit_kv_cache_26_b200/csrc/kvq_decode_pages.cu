@@ -36,9 +36,10 @@
 // eight heads, and a second product adds the lo parts.
 //
 // The newest incomplete page takes its keys from the K tail, exact 16-bit operands of the same
-// products.  W is summed in fixed point by integer atomics (units of 2^-19 of the largest weight a
-// head has met in a warp; at most 2048 tokens per warp, so no overflow): whole numbers, so the order
-// does not matter and results do not depend on timing.
+// products.  W is summed in fp32, in a fixed order (a token's turn among those of its page with the same
+// pattern is its lane's place among theirs), so results do not depend on timing.  A lane adds one
+// token for all heads of a tile at once; in the usual page few tokens share a pattern, so there are two
+// or three turns.
 #include <algorithm>
 #include <atomic>
 
@@ -52,8 +53,6 @@ namespace {
 
 constexpr int kStages = 2;   // ring stages per warp
 constexpr int kNW = 4;       // warps per CTA
-constexpr int kWarpEntries = 64;  // most list entries of a warp (the fixed-point sums hold 2048 tokens)
-constexpr int kWBits = 19;
 constexpr int kMvAhead = 64;      // pattern values in flight per thread in the final sum
 constexpr int kMaxSmem = 200 * 1024;  // dynamic, of a CTA (the largest shape, 255 patterns and 16 heads a group, takes 157 KB)
 constexpr int kPexRow = 36;       // padded row of the p exchange (floats)
@@ -132,6 +131,21 @@ __device__ __forceinline__ void split2x2(unsigned long long v, unsigned long lon
   lo[1] = half2_of(v1, w1);
 }
 
+// x[i] of the lanes of a quad (tig = 0 .. 3) exchanged, so that lane tig ends with the x[tig] of the four lanes in turn.
+__device__ __forceinline__ void quad_transpose(float (&x)[4], int tig) {
+  const bool b1 = tig & 2, b0 = tig & 1;
+  const float r0 = __shfl_xor_sync(kFull, b1 ? x[0] : x[2], 2), r1 = __shfl_xor_sync(kFull, b1 ? x[1] : x[3], 2);
+  x[0] = b1 ? r0 : x[0];
+  x[1] = b1 ? r1 : x[1];
+  x[2] = b1 ? x[2] : r0;
+  x[3] = b1 ? x[3] : r1;
+  const float s0 = __shfl_xor_sync(kFull, b0 ? x[0] : x[1], 1), s1 = __shfl_xor_sync(kFull, b0 ? x[2] : x[3], 1);
+  x[0] = b0 ? s0 : x[0];
+  x[1] = b0 ? x[1] : s0;
+  x[2] = b0 ? s1 : x[2];
+  x[3] = b0 ? x[3] : s1;
+}
+
 // Smallest row stride >= n whose rows start `step` banks apart.
 __host__ __device__ constexpr int banked(int n, int step) { return n + ((step - n) % 32 + 32) % 32; }
 
@@ -142,15 +156,14 @@ __host__ __device__ constexpr int merge_row(bool wide) { return kD + (wide ? 4 :
 struct PagesSmem {
   int bars, qk, qinv, T, W, pex, total;
   int wc, fsh, sum_o, sum_ml;  // of the merge, floats
-  int t_row, w_row;
+  int t_row;
 };
 __host__ __device__ inline PagesSmem pages_smem(int sub_bytes, int NT, bool wide, int P) {
   PagesSmem s;
   const int NH = NT * (wide ? 8 : 4);
   s.t_row = banked(P, wide ? 4 : 8);
-  s.w_row = banked(P + 1, wide ? 4 : 8);  // +1: tokens stored raw
-  // the ring; the merge at the end reuses its place: per warp and head 128 sums of p v, max, sum and unit, four sums of p z
-  s.wc = kNW * NH * merge_row(wide) + 3 * kNW * NH + kNW * NH * 4;
+  // the ring; the merge at the end reuses its place: per warp and head 128 sums of p v, max and sum, four sums of p z
+  s.wc = kNW * NH * merge_row(wide) + 2 * kNW * NH + kNW * NH * 4;
   s.fsh = s.wc + (P + kMergeRows - 1) / kMergeRows * kMergeRows * NH;
   s.sum_o = s.fsh + NH * kNW;
   s.sum_ml = s.sum_o + NH * kD;
@@ -162,9 +175,9 @@ __host__ __device__ inline PagesSmem pages_smem(int sub_bytes, int NT, bool wide
   s.qk = o; o += wide ? NH * kD * 4 : 0;      // query in the quantized space, scaled, KSC order
   s.pex = o; o += wide ? kNW * NH * kPexRow * 4 : 0;  // per-warp p exchange
   o = (o + 15) & ~15;
-  s.W = o;                                    // per-warp pattern weights; first the query in natural order (and in
+  s.W = o;                                    // per-warp pattern weights [P][NH]; first the query in natural order (and in
   const int first = NH * (kD + (wide ? 0 : kD));  // KSC order, when its users then keep it in registers)
-  o += max(kNW * NH * s.w_row, first) * 4;
+  o += max(kNW * NH * P, first) * 4;
   if (!wide) s.qk = s.W + NH * kD * 4;
   s.total = o;
   return s;
@@ -245,14 +258,16 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
   const int Gq = a.Gq, P = g.P;
   const int sub_bytes = (int)g.sub_bytes;
   const PagesSmem sp = pages_smem(sub_bytes, NT, WIDE, P);
-  const int TR = sp.t_row, WR = sp.w_row;
+  const int TR = sp.t_row;
   uint8_t* ring = smem + warp * kStages * sub_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + sp.bars) + warp * kStages;
   float* qk = reinterpret_cast<float*>(smem + sp.qk);
   float* qinv = reinterpret_cast<float*>(smem + sp.qinv);
   float* T = reinterpret_cast<float*>(smem + sp.T);
-  int* Wall = reinterpret_cast<int*>(smem + sp.W);
-  int* Ww = Wall + warp * NH * WR;
+  // pattern weights: per warp and pattern NH heads, a wide tile's even heads before its odd ones (as its lanes hold them)
+  float* Wall = reinterpret_cast<float*>(smem + sp.W);
+  float* Ww = Wall + warp * NH * P;
+  auto w_place = [](int hh) { return WIDE ? (hh & ~7) | (hh & 1) << 2 | (hh & 7) >> 1 : hh; };
   float* qn = reinterpret_cast<float*>(smem + sp.W);  // query in natural order, until T is made
   float* pex = reinterpret_cast<float*>(smem + sp.pex) + warp * NH * kPexRow;
 
@@ -430,12 +445,12 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
       for (int c = 0; c < 4; ++c) qreg[c] = reinterpret_cast<const float4*>(qk + (gq >> 1) * kD)[(2 * c + part) * 4 + tig];
     }
     __syncthreads();
-    for (int i = lane; i < NH * WR; i += 32) Ww[i] = 0;
+    for (int i = lane; i < NH / 4 * P; i += 32) reinterpret_cast<float4*>(Ww)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncwarp();
 
     // ---- per-thread state
     float accv[NT][8][4], zacc[NT][HPT][4], mrun[NT][HPT], lrun[NT][HPT], scl[NT][HPT];
-    int vexp[NT][HPT];  // accv is in units of 2^vexp, the pattern weights of 2^(vexp - kWBits); no weight p r is above 2^vexp
+    int vexp[NT][HPT];  // accv is in units of 2^vexp; no weight p r is above 2^vexp
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -619,9 +634,12 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         }
         const float4* vz4 = reinterpret_cast<const float4*>(pgp + g.off_vz) + gq;
         const float4 vz[4] = {vz4[0], vz4[8], vz4[16], vz4[24]};
-        int vi[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) vi[u] = min((int)((vidx4 >> (8 * u)) & 0xff), P);
+        // the pattern of token gq + 8 tig, and the token's turn to add its weights to the pattern's (raw tokens have none)
+        const int vi = (int)((vidx4 >> (8 * tig)) & 0xff);
+        const bool aligned = vi < Pe;
+        const unsigned alike = __match_any_sync(kFull, aligned ? vi : kRawIndex + 1 + lane);
+        const int turn = aligned ? __popc(alike & ((1u << lane) - 1u)) : 32;
+        const int turns = (int)__reduce_max_sync(kFull, aligned ? (unsigned)turn + 1u : 0u);
         // ---- online softmax (base 2), per head over the 32 tokens
         float p0[4];  // narrow: p of this lane's four V columns' tokens
 #pragma unroll
@@ -672,10 +690,34 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
                   if (!WIDE || (u & 1) == x) accv[j][mt][u] *= wfactor[x];
-              for (int jj = gq; jj < Pe; jj += 8)
-                Ww[hh * WR + jj] = __float2int_rn((float)Ww[hh * WR + jj] * wfactor[x]);
+              for (int jj = gq; jj < Pe; jj += 8) Ww[jj * NH + w_place(hh)] *= alpha[x];
             }
             __syncwarp();
+          }
+          {
+            float w[HPT][4];  // of token gq + 8 tig: the weights of the tile's heads x, x + HPT, ...
+#pragma unroll
+            for (int x = 0; x < HPT; ++x) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) w[x][u] = pv[x][u];
+              quad_transpose(w[x], tig);
+            }
+            float4* row = reinterpret_cast<float4*>(Ww + (aligned ? vi : 0) * NH + TH * j);
+            auto add = [&](int r) {
+              if (turn == r) {
+#pragma unroll
+                for (int x = 0; x < HPT; ++x) {
+                  const float4 y = row[x];
+                  row[x] = make_float4(y.x + w[x][0], y.y + w[x][1], y.z + w[x][2], y.w + w[x][3]);
+                }
+              }
+            };
+            add(0);
+#pragma unroll 1
+            for (int r = 1; r < turns; ++r) {
+              __syncwarp();
+              add(r);
+            }
           }
 #pragma unroll
           for (int x = 0; x < HPT; ++x) {
@@ -692,16 +734,6 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
               const float unit = exp2i(-vexp[j][x]);
 #pragma unroll
               for (int u = 0; u < 4; ++u) pv[x][u] *= unit;
-            }
-            {
-              constexpr float kUnits = 1 << kWBits;
-#pragma unroll
-              for (int u = 0; u < 4; u += 2) {  // rounded to whole units by the addition of 1.5 * 2^23
-                float w0, w1;
-                upk(fma2(pk(pv[x][u], pv[x][u + 1]), pk(kUnits, kUnits), pk(12582912.0f, 12582912.0f)), w0, w1);
-                atomicAdd(&Ww[hh * WR + vi[u]], __float_as_int(w0) - 0x4B400000);
-                atomicAdd(&Ww[hh * WR + vi[u + 1]], __float_as_int(w1) - 0x4B400000);
-              }
             }
             // p to the lanes of the V columns, scaled; tokens 8..15 of each 16 are columns with a factor of their own
             constexpr float f0 = kVFac, f8 = kVFac / Code<BITS>::kCol;
@@ -828,7 +860,6 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
     float* mm = mo + kNW * NH * MO;              // [kNW][NH] max
     float* ml = mm + kNW * NH;                   // [kNW][NH] sum
     float* mz = ml + kNW * NH;                   // [kNW][NH][4]
-    float* munit = mz + kNW * NH * 4;            // [kNW][NH] unit of the pattern weights
     float* wc = mo + sp.wc;                      // [P, to whole kMergeRows][NH] merged pattern weights
     float* fsh = mo + sp.fsh;                    // [NH][kNW] warp weights
 #pragma unroll
@@ -845,7 +876,6 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         if (gq == 0) {
           mm[warp * NH + hh] = mrun[j][x];
           ml[warp * NH + hh] = lrun[j][x];
-          munit[warp * NH + hh] = exp2i(vexp[j][x] - kWBits);
 #pragma unroll
           for (int u = 0; u < 4; ++u) mz[(warp * NH + hh) * 4 + u] = zacc[j][x][u];
         }
@@ -873,14 +903,12 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         else if (in_smem) sum_ml[hh] = make_float2(M, Ls);
         else if (hh < Gq) reinterpret_cast<float2*>(a.part_ml)[row0 + (int64_t)hh * a.nsplit] = make_float2(M, Ls);
       }
-#pragma unroll
-      for (int w = 0; w < kNW; ++w) f[w] *= munit[w * NH + hh];
       const int rows = (Pe + kMergeRows - 1) / kMergeRows * kMergeRows;
 #pragma unroll 4
       for (int jj = threadIdx.x / NH; jj < rows; jj += kNW * 32 / NH) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kNW; ++w) s = fmaf(f[w], (float)Wall[(w * NH + hh) * WR + min(jj, Pe - 1)], s);
+        for (int w = 0; w < kNW; ++w) s = fmaf(f[w], Wall[(w * P + min(jj, Pe - 1)) * NH + w_place(hh)], s);
         wc[jj * NH + hh] = jj < Pe ? s : 0.f;
       }
     }
@@ -1071,8 +1099,7 @@ cudaError_t launch_bits(const Geom& g, const PagesArgs& a, cudaStream_t st) {
 // Model, in units of the time a lone CTA takes for a page per warp (1.3 us on one B200): k CTAs on an SM at once take
 // max(1, 0.48 k) for a page per warp and 5 + 1.25 (k - 1) before and after the loop; the busiest SM runs its CTAs `occ` at a
 // time; merging costs a little per split, and more per head through the workspace (8 groups of 64 pages, 8 splits and 16:
-// 11.3 and 11.2 us with 4 heads a group, 13.8 and 14.8 with 8, 18.4 and 22.0 with 16).  At most kWarpEntries entries per
-// warp.  Measured with 4, 8 and 16 heads a group at 64 listed pages for 8 groups (best 8 splits; 1: 27, 39 and 60 us; 64:
+// 11.3 and 11.2 us with 4 heads a group, 13.8 and 14.8 with 8, 18.4 and 22.0 with 16).  Measured with 4, 8 and 16 heads a group at 64 listed pages for 8 groups (best 8 splits; 1: 27, 39 and 60 us; 64:
 // 18, 35 and 53), 128 groups (2) and 1024 (1), at 256 pages for 16 (16), at 128 pages for 256 (1; with 4 heads 2 are a
 // twentieth faster), at 452 pages for 3 (33): the model's choice or within a tenth of it.
 int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms) {
@@ -1081,13 +1108,11 @@ int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms) {
   const int by_regs = !wide ? 4 : Gq <= 8 ? 3 : 2;
   const int by_smem = 233472 / (pages_smem((int)g.sub_bytes, Gq > 8 ? 2 : 1, wide, g.P).total + 1024 + 128);
   const int64_t occ = std::max(1, std::min(by_regs, by_smem));
-  const int least = (int)(((int64_t)budget + kNW * kWarpEntries - 1) / (kNW * kWarpEntries));
-  const int most = std::max(least, std::min(64, budget));
+  const int most = std::min(64, budget);
   auto round = [&](int64_t k, int pages) { return 5.0 + 1.25 * (k - 1) + pages * std::max(1.0, 0.48 * k); };
-  int best = least;
+  int best = 1;
   double best_cost = 1e300;
   for (int ns = 1; ns <= most; ns = ns < 16 ? 2 * ns : ns + ns / 8) {
-    if (ns < least) continue;
     const int64_t per_sm = (units * ns + sms - 1) / sms, full = per_sm / occ, rem = per_sm % occ;
     const int pages = ((budget + ns - 1) / ns + kNW - 1) / kNW;
     const double cost = full * round(occ, pages) + (rem ? round(rem, pages) : 0.0) + 0.05 * ns + (ns >= 16 ? 0.2 * Gq : 0.0);

@@ -1,0 +1,73 @@
+"""Attention over chosen pages where weights and values span many powers of two, against float64.
+
+A dominant token of small value (an attention sink) leaves the output to the small weights of the others, so the bound of
+the error follows sum_t p_t |v_t| and not the largest weight: each logit is off by at most
+delta = 2^-20 12 scale sum_d |q_d| R_d (R the largest |k_d|), which moves the output by 2 delta S, S = sum_t p_t max |v_t|, and
+p s code, p z and W M (each below 4 |v|) are carried to 2^-20 of themselves: 2^-20 12 S."""
+import pytest
+import torch
+
+from test_serving_gpu import D, DT, G, attend, gen, key_cache, randn, rebuilt, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    import bit_kv_cache_26_b200 as m
+    return m
+
+
+def sink_cache(kvq, dt, bits, Gq, pages, at, nats, values, tx=0, sink_value=0.0):
+    """One sequence and KV head whose token `at` scores `nats` above the rest and has the value `sink_value`; the other
+    values are near one of 16 patterns, of size `values`."""
+    g, P, n = gen(pages + bits), 16, pages * G - 5
+    cache = key_cache(kvq, 1, 1, pages, dt, [0], 1, bits=bits, P=P, transform=tx, v_rho=0.3)
+    k, v = 0.05 * randn(g, n, D), torch.empty(n, D, device="cuda")
+    sign = torch.where(randn(g, D) > 0, 1.0, -1.0)
+    k[at] = sign * (nats / D ** 0.5)
+    cache.k_patterns.copy_(k[1:P + 1])
+    if tx:
+        cache.k_colscale.fill_(1.0)
+        cache.v_colscale.fill_(1.0)
+        cache.k_patterns.normal_(generator=g)
+        cache.v_patterns.normal_(generator=g)
+        v = values * randn(g, n, D)
+    else:
+        cache.v_patterns.copy_(values * randn(g, P, D))
+        pick = torch.randint(0, P, (n,), generator=g, device="cuda")
+        v = cache.v_patterns[0, 0, pick] + 0.05 * values * randn(g, n, D)
+    v[at] = sink_value
+    cache.append(k.view(1, n, 1, D).to(dt), v.view(1, n, 1, D).to(dt))
+    q = (sign + 0.02 * randn(g, 1, Gq, D)).to(dt)
+    assert cache.read_status() == 0
+    return cache, q
+
+
+def check(kvq, cache, q, order):
+    lists = torch.tensor(order, dtype=torch.int32, device="cuda").view(1, 1, -1)
+    n = torch.full((1, 1), len(order), dtype=torch.int32, device="cuda")
+    k, v = rebuilt(kvq, cache, 0)
+    assert torch.isfinite(k).all() and torch.isfinite(v).all()
+    t = (lists[0, 0].long()[:, None] * G + torch.arange(G, device="cuda")).flatten()
+    t = t[t < k.shape[0]]
+    k, v, qs, scale = k[t, 0], v[t, 0], q[0].double(), D ** -0.5
+    p = torch.softmax(qs @ k.T * scale, -1)
+    S = (p * v.abs().amax(-1)).sum(-1, keepdim=True)
+    delta = 2.0 ** -20 * 12 * scale * (qs.abs() @ k.abs().amax(0))[:, None]
+    out = attend(cache, q, lists, n)
+    assert cache.read_status(clear=True) == 0
+    within(out, (p @ v)[None], ((2 * delta + 2.0 ** -20 * 12) * S)[None])
+    return p, S
+
+
+@pytest.mark.parametrize("dtype,bits,Gq,pages,tx", [("bf16", 4, 4, 40, 0), ("fp16", 2, 3, 40, 0), ("bf16", 2, 7, 12, 0), ("fp16", 4, 16, 5, 0),
+                                                    ("bf16", 4, 1, 1, 0), ("bf16", 4, 2, 9, 1)])
+@pytest.mark.parametrize("nats", [10, 13])
+@pytest.mark.parametrize("last", [False, True])
+def test_a_dominant_token_of_no_value_leaves_the_others(kvq, dtype, bits, Gq, pages, tx, nats, last):
+    at = (pages - 1) * G + 9 if last else 0
+    cache, q = sink_cache(kvq, DT[dtype], bits, Gq, pages, at, nats, 1.0, tx)
+    for order in (list(range(pages)), list(range(pages))[::-1]):
+        p, _ = check(kvq, cache, q, order)
+        assert float(p.max(-1).values.min()) > 0.9 or nats < 13      # the sink has most of the weight
