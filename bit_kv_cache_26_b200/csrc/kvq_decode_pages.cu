@@ -26,8 +26,12 @@
 // half word (S <= 6, so it fits the ten mantissa bits), which the tensor cores multiply exactly.
 // One AND per pair of codes; the powers of two of the four fields of a 16x16 tile separate into a
 // row factor (undone on the sums) and a column factor (folded into B).  B is q s or p s in fp16
-// hi + lo parts (22 bits), from a query scaled by a power of two to [16, 32): scales up to 2000 for K
-// and 1000 for V fit fp16; past them the output is not finite and KVQ_DEV_RANGE is set.
+// hi + lo parts (22 bits).  The query is scaled by a power of two to [16, 32): K scales up to 2000 fit
+// fp16 (past them the output is not finite and KVQ_DEV_RANGE is set); of a product too small for hi + lo
+// 2^-25 is dropped, as if the key's scale were off by 2^-29 (2^-25 in columns with a factor).  p s is in units that follow the largest
+// product a head has met in the warp (below 2^15 of them), so that a dominant token of small value, or
+// values that are small throughout, leave the others their bits: what is dropped is 2^-33 of that
+// product (2^-29 where columns have a factor).
 //
 // Up to four query heads per KV head: the eight columns of a product are (head, {hi, lo}).  The two
 // lanes of a head's columns each form the products of half the channels (tokens for V) and give each
@@ -56,7 +60,9 @@ constexpr int kNW = 4;       // warps per CTA
 constexpr int kMvAhead = 64;      // pattern values in flight per thread in the final sum
 constexpr int kMaxSmem = 200 * 1024;  // dynamic, of a CTA (the largest shape, 255 patterns and 16 heads a group, takes 157 KB)
 constexpr int kPexRow = 36;       // padded row of the p exchange (floats)
-constexpr float kVFac = 64.0f;    // p s is scaled by it before fp16
+constexpr int kVTop = 15;         // p s, as an fp16 operand, is below 2^kVTop
+constexpr int kVRoom = 3;         // powers of two of room for the products to come when the unit is set, and again before it is lowered
+constexpr float kVLeast = 7.8886091e-31f;  // 2^-100: V scales below it do not set the operands' unit
 
 template <int BITS>
 struct Code {
@@ -96,9 +102,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 2^e, to the range of normal numbers; the smallest power of two above a number >= 0 (or one below all normal ones).
+// 2^e, to the range of normal numbers.
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + max(-126, min(127, e))) << 23); }
-__device__ __forceinline__ int exponent_above(float x) { return (int)(__float_as_uint(x) >> 23 & 0xff) - 126; }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // e of a normal number
+// 2^e / x of a power of two x.
+__device__ __forceinline__ float pow2_over(int e, float x) { return __uint_as_float(((uint32_t)(254 + e) << 23) - __float_as_uint(x)); }
+// x's exponent: x < 2^(exponent(x) + 1) for a number x >= 0.
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 0xff) - 127; }
 
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   uint32_t h;
@@ -450,14 +460,17 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 
     // ---- per-thread state
     float accv[NT][8][4], zacc[NT][HPT][4], mrun[NT][HPT], lrun[NT][HPT], scl[NT][HPT];
-    int vexp[NT][HPT];  // accv is in units of 2^vexp; no weight p r is above 2^vexp
+    // accv is in units of 2^-kVTop vlim, a power of two above all products p r s so far; vtop: the largest when it was set, as it
+    // has shrunk since
+    float vlim[NT][HPT], vtop[NT][HPT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int x = 0; x < HPT; ++x) {
         mrun[j][x] = -INFINITY;
         lrun[j][x] = 0.f;
-        vexp[j][x] = TX ? -100 : 0;  // (without row factors a weight is at most 1)
+        vlim[j][x] = pow2(-100);
+        vtop[j][x] = 0.f;
         scl[j][x] = a.scale_log2 * qinv[TH * j + HPT * tig + x];
 #pragma unroll
         for (int u = 0; u < 4; ++u) zacc[j][x][u] = 0.f;
@@ -640,11 +653,18 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         const unsigned alike = __match_any_sync(kFull, aligned ? vi : kRawIndex + 1 + lane);
         const int turn = aligned ? __popc(alike & ((1u << lane) - 1u)) : 32;
         const int turns = (int)__reduce_max_sync(kFull, aligned ? (unsigned)turn + 1u : 0u);
+        // the largest V scale of token gq + 8 tig, and of the page
+        float vmax;
+        {
+          const float4 v = reinterpret_cast<const float4*>(pgp + g.off_vs)[((tig >> 1) * 4 + (gq & 1) + 2 * (tig & 1)) * 4 + (gq >> 1)];
+          vmax = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+        }
+        const float page_vmax = fmaxf(__uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vmax))), kVLeast);
         // ---- online softmax (base 2), per head over the 32 tokens
         float p0[4];  // narrow: p of this lane's four V columns' tokens
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          float pv[HPT][4], p[HPT][4], alpha[HPT], wfactor[HPT];
+          float pv[HPT][4], p[HPT][4], alpha[HPT], top[HPT], wfactor[HPT];
           bool same = true;
 #pragma unroll
           for (int x = 0; x < HPT; ++x) {
@@ -664,21 +684,34 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
               pv[x][u] = TX ? p[x][u] * vrow[u] : p[x][u];
               pv[x][u + 1] = TX ? p[x][u + 1] * vrow[u + 1] : p[x][u + 1];
             }
-            wfactor[x] = alpha[x];
-            if constexpr (TX) {
-              // p r has no bound of its own: the unit follows the largest so far, as far as that still counts
-              float most = fmaxf(fmaxf(pv[x][0], pv[x][1]), fmaxf(pv[x][2], pv[x][3]));
-              most = fmaxf(most, __shfl_xor_sync(kFull, most, 4));
-              most = fmaxf(most, __shfl_xor_sync(kFull, most, 8));
-              most = fmaxf(most, __shfl_xor_sync(kFull, most, 16));
-              const int now = exponent_above(most), was = vexp[j][x] + (alpha[x] == 1.0f ? 0 : exponent_above(alpha[x]));
-              const int e = max(-100, min(100, max(now, was)));
-              wfactor[x] *= exp2i(vexp[j][x] - e);
-              vexp[j][x] = e;
-            }
-            same = same && alpha[x] == 1.0f && wfactor[x] == 1.0f;
+            // (the page's largest scale stands for each token's until that is not good enough)
+            top[x] = fmaxf(fmaxf(pv[x][0], pv[x][1]), fmaxf(pv[x][2], pv[x][3])) * page_vmax;
+            same = same && alpha[x] == 1.0f && top[x] < vlim[j][x];
           }
           if (!__all_sync(kFull, same)) {
+            bool unit_fits = true;
+#pragma unroll
+            for (int x = 0; x < HPT; ++x) {
+              vtop[j][x] *= alpha[x];
+              unit_fits = unit_fits && top[x] < vlim[j][x] && vtop[j][x] * (2 << 2 * kVRoom) >= vlim[j][x];
+              wfactor[x] = alpha[x];
+            }
+            if (!__all_sync(kFull, unit_fits)) {
+              // the units of the heads follow their largest products so far, as far as those still count
+#pragma unroll
+              for (int x = 0; x < HPT; ++x) {
+                float most = vtop[j][x];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) most = fmaxf(most, pv[x][u] * fmaxf(__shfl_sync(kFull, vmax, (lane & ~3) + u), kVLeast));
+                most = fmaxf(most, __shfl_xor_sync(kFull, most, 4));
+                most = fmaxf(most, __shfl_xor_sync(kFull, most, 8));
+                most = fmaxf(most, __shfl_xor_sync(kFull, most, 16));
+                const int old = exponent(vlim[j][x]), e = max(-100, min(100, exponent(most) + 1 + kVRoom));
+                vlim[j][x] = pow2(e);
+                vtop[j][x] = most;
+                wfactor[x] *= exp2i(old - e);
+              }
+            }
 #pragma unroll
             for (int x = 0; x < HPT; ++x) {
               const int hh = TH * j + HPT * tig + x;
@@ -730,13 +763,8 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
               zacc[j][x][2] = fmaf(pv[x][u], vz[u].z, zacc[j][x][2]);
               zacc[j][x][3] = fmaf(pv[x][u], vz[u].w, zacc[j][x][3]);
             }
-            if constexpr (TX) {
-              const float unit = exp2i(-vexp[j][x]);
-#pragma unroll
-              for (int u = 0; u < 4; ++u) pv[x][u] *= unit;
-            }
             // p to the lanes of the V columns, scaled; tokens 8..15 of each 16 are columns with a factor of their own
-            constexpr float f0 = kVFac, f8 = kVFac / Code<BITS>::kCol;
+            const float f0 = pow2_over(kVTop, vlim[j][x]), f8 = f0 / Code<BITS>::kCol;
             if constexpr (WIDE) {
               float y[4];
               upk(mul2(pk(pv[x][0], pv[x][1]), pk(f0, f8)), y[0], y[1]);
@@ -867,7 +895,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
 #pragma unroll
       for (int x = 0; x < HPT; ++x) {
         const int hh = TH * j + HPT * tig + x;
-        const float f0 = 16777216.0f / kVFac * (TX ? exp2i(vexp[j][x]) : 1.0f), f8 = f0 / Code<BITS>::kRow;
+        const float f0 = vlim[j][x] * pow2(24 - kVTop), f8 = f0 / Code<BITS>::kRow;
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
           mo[(warp * NH + hh) * MO + 16 * mt + gq] = (WIDE ? accv[j][mt][x] : accv[j][mt][0] + accv[j][mt][1]) * f0;

@@ -407,9 +407,10 @@ KVQ_API kvq_status kvq_select_pages(const kvq_cache* cache, const void* q, int32
  *   q, out [num_seqs][num_q_heads][128] dtype: unlike kvq_decode_attention's, `out` is in the
  *   cache's dtype (softmax and sums in fp32, rounded once).  No entries: zeros.
  * NaN in a query shows in its head's output.  The same inputs give the same bits on every run.
- * K scales above about 2000 and V scales above about 1000 leave the operands' range
- * (KVQ_DEV_RANGE).  A page copy that does not arrive within the bounded wait flags
- * KVQ_DEV_TIMEOUT.
+ * K scales above about 2000 leave the operands' range (KVQ_DEV_RANGE); logits are off by at most
+ * 2^-17 sm_scale max |q_d| (of the transformed query under the pre-transform) beside fp32's own
+ * rounding, and values by 2^-29 of the largest weight x V scale.  A page copy that does not arrive
+ * within the bounded wait flags KVQ_DEV_TIMEOUT.
  * Workspace: kvq_decode_pages_workspace_bytes(), 256-byte aligned, ZERO-FILLED before its first use
  * (its counters are left at zero again).  Two calls in flight at once on one workspace race.
  */

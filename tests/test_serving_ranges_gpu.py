@@ -63,7 +63,7 @@ def check(kvq, cache, q, order):
 
 @pytest.mark.parametrize("dtype,bits,Gq,pages,tx", [("bf16", 4, 4, 40, 0), ("fp16", 2, 3, 40, 0), ("bf16", 2, 7, 12, 0), ("fp16", 4, 16, 5, 0),
                                                     ("bf16", 4, 1, 1, 0), ("bf16", 4, 2, 9, 1)])
-@pytest.mark.parametrize("nats", [10, 13])
+@pytest.mark.parametrize("nats", [10, 13, 16])
 @pytest.mark.parametrize("last", [False, True])
 def test_a_dominant_token_of_no_value_leaves_the_others(kvq, dtype, bits, Gq, pages, tx, nats, last):
     at = (pages - 1) * G + 9 if last else 0
@@ -71,3 +71,29 @@ def test_a_dominant_token_of_no_value_leaves_the_others(kvq, dtype, bits, Gq, pa
     for order in (list(range(pages)), list(range(pages))[::-1]):
         p, _ = check(kvq, cache, q, order)
         assert float(p.max(-1).values.min()) > 0.9 or nats < 13      # the sink has most of the weight
+
+
+@pytest.mark.parametrize("dtype,bits,Gq,pages,tx", [("bf16", 4, 4, 40, 0), ("bf16", 2, 7, 12, 0), ("fp16", 2, 4, 40, 0), ("bf16", 2, 12, 5, 0),
+                                                    ("bf16", 4, 2, 9, 1)])
+@pytest.mark.parametrize("values,nats", [(1e-5, 0), (1e-6, 12), (1e-3, 14), (1e-3, 20), (3e-5, 16), (6e4, 0), (3e4, 12)])
+def test_small_and_large_values_keep_their_bits(kvq, dtype, bits, Gq, pages, tx, values, nats):
+    if dtype == "fp16":
+        values = min(max(values, 1e-3), 1e3)                         # what the type holds, and what the reconstruction must stay below
+    cache, q = sink_cache(kvq, DT[dtype], bits, Gq, pages, 0, nats, values, tx)
+    for order in (list(range(pages)), list(range(pages))[::-1]):
+        check(kvq, cache, q, order)
+    if bits == 2 and values == 6e4 and tx == 0:                      # scales that no fp16 holds
+        at = 2 * (G * D * bits // 8) + 1024
+        assert float(cache.subblock(0, 1, 0)[at:at + 512].view(torch.float32).max()) > 2000
+
+
+def test_pages_of_very_different_values(kvq):
+    # pages whose values are 2^-20 .. 2^20 times the others', in both orders and alone
+    cache, q = sink_cache(kvq, torch.bfloat16, 4, 5, 6, 0, 0, 1.0)
+    at = 2 * (G * D * 4 // 8) + 1024
+    for page, f in ((1, 2.0 ** -20), (3, 2.0 ** 20), (4, 2.0 ** -60)):
+        sub = cache.subblock(0, page, 0)
+        sub[at:at + 1024].view(torch.float32).mul_(f)                # scales and zeros
+        sub[at + 1056:at + 1088] = 255                               # without patterns
+    for order in ([0, 1, 2, 3, 4, 5], [3, 1, 0], [1, 4], [4], [1, 0], [5, 4, 3, 2, 1, 0]):
+        check(kvq, cache, q, order)
