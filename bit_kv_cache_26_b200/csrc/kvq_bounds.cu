@@ -395,8 +395,7 @@ __global__ void __launch_bounds__(kSelThreads, 6) select_pages_kernel(Geom g, Se
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-      last = atomicAdd(a.arrivals + grp, 1) == a.nsplit - 1;
-      if (last) a.arrivals[grp] = 0;  // ready for the next call
+      last = arrive_last(a.counters, grp, a.counter_bits, a.nsplit);
     }
     __syncthreads();
     if (!last) return;
@@ -431,19 +430,17 @@ cudaError_t launch_page_bounds(const Geom& g, const void* k_new, int n_new, void
   return cudaGetLastError();
 }
 
-// Arrival counters (first, so that their place does not depend on anything but the cache), then the keys.
-size_t select_workspace(const Geom& g) {
-  const size_t groups = (size_t)g.B * g.H;
-  return (groups * sizeof(int) + 255) / 256 * 256 + groups * (size_t)g.maxp * sizeof(uint32_t);
-}
+// Arrival counters, then the keys.
+size_t select_workspace(const Geom& g) { return kCounterBytes + (size_t)g.B * g.H * (size_t)g.maxp * sizeof(uint32_t); }
 
 cudaError_t launch_select(const Geom& g, SelectArgs a, void* ws, int num_sms, cudaStream_t st) {
   const size_t groups = (size_t)g.B * g.H;
   a.minus_zero = -0.0f;
-  a.arrivals = (int*)ws;
-  a.keys = (uint32_t*)((uint8_t*)ws + (groups * sizeof(int) + 255) / 256 * 256);
+  a.counters = (unsigned*)ws;
+  a.counter_bits = counter_bits((int64_t)groups);
+  a.keys = (uint32_t*)((uint8_t*)ws + kCounterBytes);
   // as many CTAs as six per SM, each with 32 pages (one round of its warps) or more
-  const int64_t most = std::max(1, g.maxp / 32);
+  const int64_t most = std::min<int64_t>(std::max(1, g.maxp / 32), a.counter_bits ? (INT64_C(1) << a.counter_bits) - 1 : 1);
   a.nsplit = (int)std::min<int64_t>(most, std::max<int64_t>(1, 6 * (int64_t)num_sms / (int64_t)groups));
   const dim3 grid(a.nsplit, g.H, g.B);
   auto* kernel = g.dtype == KVQ_BF16 ? select_pages_kernel<true> : select_pages_kernel<false>;

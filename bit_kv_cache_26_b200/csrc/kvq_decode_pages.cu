@@ -1041,8 +1041,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    last = atomicAdd(a.arrivals + grp, 1) == a.nsplit - 1;
-    if (last) a.arrivals[grp] = 0;  // ready for the next call
+    last = arrive_last(a.counters, grp, a.counter_bits, a.nsplit);
   }
   __syncthreads();
   if (!last) return;
@@ -1136,7 +1135,8 @@ int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms) {
   const int by_regs = !wide ? 4 : Gq <= 8 ? 3 : 2;
   const int by_smem = 233472 / (pages_smem((int)g.sub_bytes, Gq > 8 ? 2 : 1, wide, g.P).total + 1024 + 128);
   const int64_t occ = std::max(1, std::min(by_regs, by_smem));
-  const int most = std::min(64, budget);
+  // (through the workspace only where the groups' counters hold the splits, which no group count past 256 wants)
+  const int most = std::min(counter_bits(units) >= 8 ? 64 : 8, budget);
   auto round = [&](int64_t k, int pages) { return 5.0 + 1.25 * (k - 1) + pages * std::max(1.0, 0.48 * k); };
   int best = 1;
   double best_cost = 1e300;
@@ -1149,11 +1149,9 @@ int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms) {
   return best;
 }
 
-static size_t counters_bytes(const Geom& g) { return ((size_t)g.B * g.H * sizeof(int) + 255) / 256 * 256; }
-
-// Arrival counters first (their place depends on the cache alone), then the partials.
+// Arrival counters, then the partials.
 size_t decode_pages_workspace(const Geom& g, int Hq, int nsplit) {
-  return counters_bytes(g) + (size_t)g.B * Hq * nsplit * (2 + kD) * sizeof(float);
+  return kCounterBytes + (size_t)g.B * Hq * nsplit * (2 + kD) * sizeof(float);
 }
 
 cudaError_t launch_decode_pages(const Geom& g0, PagesArgs a, void* ws, cudaStream_t st) {
@@ -1162,9 +1160,10 @@ cudaError_t launch_decode_pages(const Geom& g0, PagesArgs a, void* ws, cudaStrea
   // 64 groups of 64 pages, 4 splits: 17.1 us as clusters, 20.8 us through the workspace; 8 groups, 8 splits: 11.1 / 13.6 us;
   // 16 splits measured the same either way
   a.clustered = a.nsplit == 2 || a.nsplit == 4 || a.nsplit == 8;
-  a.arrivals = (int*)ws;
+  a.counters = (unsigned*)ws;
+  a.counter_bits = counter_bits((int64_t)g.B * g.H);
   // the rows of 128 first: they are read 16 bytes at a time, which an odd number of (max, sum) pairs before them would not allow
-  a.part_o = (float*)((uint8_t*)ws + counters_bytes(g));
+  a.part_o = (float*)((uint8_t*)ws + kCounterBytes);
   a.part_ml = a.part_o + kD * (size_t)g.B * a.Hq * a.nsplit;
   if (g.tx) return g.bits == 2 ? launch_bits<2, true>(g, a, st) : launch_bits<4, true>(g, a, st);
   return g.bits == 2 ? launch_bits<2, false>(g, a, st) : launch_bits<4, false>(g, a, st);

@@ -45,7 +45,8 @@ struct PagesArgs {
   uint16_t* out;
   float* part_ml;
   float* part_o;
-  int* arrivals;
+  unsigned* counters;
+  int counter_bits;
 };
 int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms);
 size_t decode_pages_workspace(const Geom& g, int Hq, int nsplit);
@@ -60,9 +61,9 @@ struct SelectArgs {
   int budget, sink, recent;
   int32_t* list;
   int32_t* list_len;
-  int* arrivals;
+  unsigned* counters;
   uint32_t* keys;
-  int nsplit;
+  int nsplit, counter_bits;
   float minus_zero;
 };
 size_t select_workspace(const Geom& g);

@@ -1,5 +1,5 @@
-// Asynchronous page copies (cp.async.bulk tracked by mbarriers with bounded waits) and packed
-// fp32 pairs, shared by the kernels that attend over the paged cache.
+// Asynchronous page copies (cp.async.bulk tracked by mbarriers with bounded waits), packed fp32
+// pairs and arrival counters, shared by the kernels that attend over the paged cache.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -39,6 +39,20 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t phase, uint32_
     if (ok) return true;
   }
   return false;
+}
+
+// The arrival counters of a workspace: its first kCounterBytes, zero between calls.  No call keeps anything else there,
+// whatever the shape, so that one workspace serves calls of different shapes in turn.  A group's counter has `bits` bits of
+// its word: 32 for up to 64 groups, 16, 8 and 4 for up to 128, 256 and 512 (0: more groups have none).
+constexpr int kCounterBytes = 256;
+inline int counter_bits(int64_t groups) { return groups <= 64 ? 32 : groups <= 128 ? 16 : groups <= 256 ? 8 : groups <= 512 ? 4 : 0; }
+// One arrival of the n < 2^bits of group grp: true for the last, which leaves the counter at zero.
+__device__ __forceinline__ bool arrive_last(unsigned* counters, int64_t grp, int bits, unsigned n) {
+  const int per = 32 / bits, shift = (int)(grp % per) * bits;
+  unsigned* word = counters + grp / per;
+  const bool last = (atomicAdd(word, 1u << shift) >> shift & (0xffffffffu >> (32 - bits))) == n - 1u;
+  if (last) atomicSub(word, n << shift);
+  return last;
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -14,6 +14,7 @@
 
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
+#include "kvq_pipe.cuh"
 
 namespace kvq {
 
@@ -24,6 +25,7 @@ constexpr int kPlanOnce = 2048;       // up to so many sequences every CTA makes
 constexpr int kOnceCtas = 4;          // CTAs per SM then, at most
 constexpr int kPlanAhead = 2;         // rounds of a chunk (two tokens per thread each)
 constexpr int kPlanScan = 1024;       // threads of the scan when it is a launch of its own
+constexpr int kPlanData = kCounterBytes / 4;  // words of the workspace before the scan's results
 
 __device__ __forceinline__ longlong2 add2ll(longlong2 a, longlong2 b) { return make_longlong2(a.x + b.x, a.y + b.y); }
 
@@ -207,7 +209,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_once_kernel(Geom g, PlanArg
 }
 
 // More sequences, two launches: one CTA makes the scans, cu_new, the pages before each sequence (workspace) and the free
-// count left; then the tokens.  Workspace: [1] free ids at the start, [2] tokens of the plan, [4 + b] new pages before b.
+// count left; then the tokens.  Workspace, past the counters: [0] free ids at the start, [1] tokens of the plan, [2 + b] new
+// pages before b.
 __global__ void __launch_bounds__(kPlanScan) plan_scan_kernel(Geom g, PlanArgs a) {
   __shared__ longlong2 warp_tot[32];
   __shared__ longlong2 s_tot;
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kPlanScan) plan_scan_kernel(Geom g, PlanArgs a
     const bool served = b < g.B && upto.x <= a.max_tokens && upto.y <= free_n;
     if (served) {
       a.cu[b + 1] = (int32_t)upto.x;
-      a.ws[4 + b] = (int32_t)(upto.y - mine.y);
+      a.ws[kPlanData + 2 + b] = (int32_t)(upto.y - mine.y);
     } else if (mine.x > 0) {
       set_status(g.status, upto.y > free_n ? KVQ_DEV_NO_PAGES : KVQ_DEV_OVERFLOW);
     }
@@ -245,12 +248,12 @@ __global__ void __launch_bounds__(kPlanScan) plan_scan_kernel(Geom g, PlanArgs a
   const longlong2 tot = s_tot;
   for (int b = n_served + tid; b < g.B; b += blockDim.x) {
     a.cu[b + 1] = (int32_t)tot.x;
-    a.ws[4 + b] = (int32_t)tot.y;
+    a.ws[kPlanData + 2 + b] = (int32_t)tot.y;
   }
   if (tid == 0) {
     a.cu[0] = 0;
-    a.ws[1] = (int32_t)free_n;
-    a.ws[2] = (int32_t)tot.x;
+    a.ws[kPlanData] = (int32_t)free_n;
+    a.ws[kPlanData + 1] = (int32_t)tot.x;
     *a.free_left = (int32_t)(free_n - tot.y);
   }
 }
@@ -258,19 +261,19 @@ __global__ void __launch_bounds__(kPlanScan) plan_scan_kernel(Geom g, PlanArgs a
 __global__ void __launch_bounds__(kPlanThreads) plan_expand_kernel(Geom g, PlanArgs a, int chunk) {
   __shared__ int s_range[2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int total = a.ws[2];
+  const int total = a.ws[kPlanData + 1];
   const int64_t begin = (int64_t)blockIdx.x * chunk;
   if (begin >= total) return;
   const int end = (int)min((int64_t)total, begin + chunk);
   if (threadIdx.x < 2)  // the sequences of the chunk's first and last token
     s_range[threadIdx.x] = seq_of(a.cu, threadIdx.x ? end - 1 : (int)begin, 0, g.B - 1);
   __syncthreads();
-  expand(g, a, a.cu, a.ws + 4, g.seq_len, (int)begin, end, s_range[0], s_range[1], a.ws[1]);
+  expand(g, a, a.cu, a.ws + kPlanData + 2, g.seq_len, (int)begin, end, s_range[0], s_range[1], a.ws[kPlanData]);
 }
 
 }  // namespace
 
-size_t plan_workspace(const Geom& g) { return ((size_t)g.B + 4) * sizeof(int32_t); }
+size_t plan_workspace(const Geom& g) { return ((size_t)g.B + 4 + (g.B > kPlanOnce ? kPlanData : 0)) * sizeof(int32_t); }
 
 cudaError_t launch_plan(const Geom& g, const PlanArgs& a, int num_sms, cudaStream_t st) {
   constexpr int chunk = 2 * kPlanThreads * kPlanAhead;  // tokens of a CTA at a time

@@ -300,7 +300,8 @@ KVQ_API kvq_status kvq_decode_attention_static(const kvq_cache* cache, const voi
  * Workspace: kvq_step_workspace_bytes(), 256-byte aligned, ZERO-FILLED before its first use:
  * besides the split partials it holds counters that every call leaves at zero again (no memset
  * per step, so a step can be captured in a CUDA graph as one kernel node).  Two steps in flight
- * at once on one workspace race.
+ * at once on one workspace race.  The counters' place depends on the cache's sizes and num_q_heads:
+ * a workspace used with others is zeroed again first.
  */
 KVQ_API size_t kvq_step_workspace_bytes(const kvq_cache* cache, int32_t num_q_heads);
 KVQ_API kvq_status kvq_decode_step(const kvq_cache* cache, const void* k_new, const void* v_new, const void* q,
@@ -355,8 +356,9 @@ KVQ_API kvq_status kvq_norm_rope(const kvq_rows* q, const kvq_rows* k, const kvq
  * When the tokens would pass max_tokens (KVQ_DEV_OVERFLOW) or the pages the stack
  * (KVQ_DEV_NO_PAGES), that sequence and all after it get nothing.
  * slot_map, positions and seq_ids are 16-byte aligned.
- * Workspace: kvq_plan_workspace_bytes(), 4-byte aligned, ZERO-FILLED before its first use (its counter is left at
- * zero again).  Two calls in flight at once on one workspace race.
+ * Workspace: kvq_plan_workspace_bytes(), 4-byte aligned, ZERO-FILLED before its first use (its counters are left at
+ * zero again).  One workspace, zeroed once, serves calls of any shapes in turn that it is large enough for, and
+ * kvq_select_pages and kvq_decode_attention_pages too; two calls in flight at once on one workspace race.
  */
 KVQ_API size_t kvq_plan_workspace_bytes(const kvq_cache* cache);
 KVQ_API kvq_status kvq_plan_pages(const kvq_cache* cache, const int32_t* new_len, const int32_t* free_pages,
@@ -391,7 +393,8 @@ KVQ_API kvq_status kvq_page_bounds(const kvq_cache* cache, const void* k_new, in
  *   list_len  [num_seqs][num_kv_heads] int32
  * 1 <= recent, 0 <= sink, sink + recent <= budget.
  * Workspace: kvq_select_workspace_bytes(), 256-byte aligned, ZERO-FILLED before its first use (its
- * counters are left at zero again).  Two calls in flight at once on one workspace race.
+ * counters are left at zero again).  As with kvq_plan_pages it serves any shapes in turn; two calls
+ * in flight at once on one workspace race.
  */
 KVQ_API size_t kvq_select_workspace_bytes(const kvq_cache* cache);
 KVQ_API kvq_status kvq_select_pages(const kvq_cache* cache, const void* q, int32_t num_q_heads, const void* bounds,
@@ -412,7 +415,8 @@ KVQ_API kvq_status kvq_select_pages(const kvq_cache* cache, const void* q, int32
  * rounding, and values by 2^-29 of the largest weight x V scale.  A page copy that does not arrive
  * within the bounded wait flags KVQ_DEV_TIMEOUT.
  * Workspace: kvq_decode_pages_workspace_bytes(), 256-byte aligned, ZERO-FILLED before its first use
- * (its counters are left at zero again).  Two calls in flight at once on one workspace race.
+ * (its counters are left at zero again).  As with kvq_plan_pages it serves any shapes in turn; two
+ * calls in flight at once on one workspace race.
  */
 KVQ_API size_t kvq_decode_pages_workspace_bytes(const kvq_cache* cache, int32_t num_q_heads, int32_t budget);
 KVQ_API kvq_status kvq_decode_attention_pages(const kvq_cache* cache, const void* q, int32_t num_q_heads,
