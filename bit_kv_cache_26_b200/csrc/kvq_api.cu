@@ -389,7 +389,7 @@ kvq_status kvq_select_pages(const kvq_cache* cache, const void* q, int32_t num_q
 size_t kvq_decode_pages_workspace_bytes(const kvq_cache* cache, int32_t num_q_heads, int32_t budget) {
   if (!cache || num_q_heads < 1 || cache->num_kv_heads < 1 || cache->num_seqs < 0 || budget < 1) return 0;
   kvq::Geom g = kvq::make_geom(*cache);
-  return kvq::decode_pages_workspace(g, num_q_heads, kvq::decode_pages_splits(g, num_q_heads / cache->num_kv_heads, budget, num_sms()));
+  return kvq::decode_pages_workspace(g, num_q_heads, kvq::decode_pages_most_splits(g, num_q_heads / cache->num_kv_heads, budget, num_sms()));
 }
 
 kvq_status kvq_decode_attention_pages(const kvq_cache* cache, const void* q, int32_t num_q_heads, float sm_scale,
@@ -415,7 +415,7 @@ kvq_status kvq_decode_attention_pages(const kvq_cache* cache, const void* q, int
   a.budget = budget;
   a.nsplit = kvq::decode_pages_splits(g, a.Gq, budget, num_sms());
   a.out = (uint16_t*)out;
-  const size_t need = kvq::decode_pages_workspace(g, num_q_heads, a.nsplit);
+  const size_t need = kvq::decode_pages_need(g, num_q_heads, a.nsplit);
   if (ws_bytes < need || !ws) return fail(KVQ_ERR_WORKSPACE, "decode workspace %zu < %zu bytes", ws_bytes, need);
   if (!aligned(ws, 256)) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   cudaError_t e = kvq::launch_decode_pages(g, a, ws, (cudaStream_t)stream);

@@ -1129,29 +1129,49 @@ cudaError_t launch_bits(const Geom& g, const PagesArgs& a, cudaStream_t st) {
 // 11.3 and 11.2 us with 4 heads a group, 13.8 and 14.8 with 8, 18.4 and 22.0 with 16).  Measured with 4, 8 and 16 heads a group at 64 listed pages for 8 groups (best 8 splits; 1: 27, 39 and 60 us; 64:
 // 18, 35 and 53), 128 groups (2) and 1024 (1), at 256 pages for 16 (16), at 128 pages for 256 (1; with 4 heads 2 are a
 // twentieth faster), at 452 pages for 3 (33): the model's choice or within a tenth of it.
-int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms) {
+// The budget is rounded up to eight sizes per power of two first, so that the largest choice of all budgets up to one is
+// found by trying few.
+static int64_t rounded_budget(int64_t budget) {
+  int64_t step = 1;
+  while (16 * step < budget) step *= 2;
+  return (budget + step - 1) / step * step;
+}
+int decode_pages_splits(const Geom& g, int Gq, int budget_, int num_sms) {
+  const int64_t budget = rounded_budget(budget_);
   const int64_t units = std::max<int64_t>(1, (int64_t)g.B * g.H), sms = std::max(1, num_sms);
   const bool wide = Gq > 4;
   const int by_regs = !wide ? 4 : Gq <= 8 ? 3 : 2;
   const int by_smem = 233472 / (pages_smem((int)g.sub_bytes, Gq > 8 ? 2 : 1, wide, g.P).total + 1024 + 128);
   const int64_t occ = std::max(1, std::min(by_regs, by_smem));
   // (through the workspace only where the groups' counters hold the splits, which no group count past 256 wants)
-  const int most = std::min(counter_bits(units) >= 8 ? 64 : 8, budget);
-  auto round = [&](int64_t k, int pages) { return 5.0 + 1.25 * (k - 1) + pages * std::max(1.0, 0.48 * k); };
+  const int most = (int)std::min<int64_t>(counter_bits(units) >= 8 ? 64 : 8, budget);
+  auto round = [&](int64_t k, int64_t pages) { return 5.0 + 1.25 * (k - 1) + pages * std::max(1.0, 0.48 * k); };
   int best = 1;
   double best_cost = 1e300;
   for (int ns = 1; ns <= most; ns = ns < 16 ? 2 * ns : ns + ns / 8) {
     const int64_t per_sm = (units * ns + sms - 1) / sms, full = per_sm / occ, rem = per_sm % occ;
-    const int pages = ((budget + ns - 1) / ns + kNW - 1) / kNW;
+    const int64_t pages = ((budget + ns - 1) / ns + kNW - 1) / kNW;
     const double cost = full * round(occ, pages) + (rem ? round(rem, pages) : 0.0) + 0.05 * ns + (ns >= 16 ? 0.2 * Gq : 0.0);
     if (cost < best_cost * (1.0 - 1e-9)) { best_cost = cost; best = ns; }
   }
   return best;
 }
 
-// Arrival counters, then the partials.
+int decode_pages_most_splits(const Geom& g, int Gq, int budget, int num_sms) {
+  int most = 1;
+  for (int64_t b = 1; b <= rounded_budget(budget); b = rounded_budget(b + 1))
+    most = std::max(most, decode_pages_splits(g, Gq, (int)std::min<int64_t>(b, budget), num_sms));
+  return most;
+}
+
+static bool meet_in_clusters(int nsplit) { return nsplit == 2 || nsplit == 4 || nsplit == 8; }
+
+// Arrival counters, then the partials of the splits that meet in the workspace.
 size_t decode_pages_workspace(const Geom& g, int Hq, int nsplit) {
   return kCounterBytes + (size_t)g.B * Hq * nsplit * (2 + kD) * sizeof(float);
+}
+size_t decode_pages_need(const Geom& g, int Hq, int nsplit) {
+  return nsplit == 1 || meet_in_clusters(nsplit) ? (size_t)kCounterBytes : decode_pages_workspace(g, Hq, nsplit);
 }
 
 cudaError_t launch_decode_pages(const Geom& g0, PagesArgs a, void* ws, cudaStream_t st) {
@@ -1159,7 +1179,7 @@ cudaError_t launch_decode_pages(const Geom& g0, PagesArgs a, void* ws, cudaStrea
   g.wait_limit = page_wait_limit(g0.wait_limit);
   // 64 groups of 64 pages, 4 splits: 17.1 us as clusters, 20.8 us through the workspace; 8 groups, 8 splits: 11.1 / 13.6 us;
   // 16 splits measured the same either way
-  a.clustered = a.nsplit == 2 || a.nsplit == 4 || a.nsplit == 8;
+  a.clustered = meet_in_clusters(a.nsplit);
   a.counters = (unsigned*)ws;
   a.counter_bits = counter_bits((int64_t)g.B * g.H);
   // the rows of 128 first: they are read 16 bytes at a time, which an odd number of (max, sum) pairs before them would not allow

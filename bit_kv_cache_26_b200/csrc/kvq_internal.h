@@ -49,7 +49,9 @@ struct PagesArgs {
   int counter_bits;
 };
 int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms);
+int decode_pages_most_splits(const Geom& g, int Gq, int budget, int num_sms);  // of all budgets up to this one
 size_t decode_pages_workspace(const Geom& g, int Hq, int nsplit);
+size_t decode_pages_need(const Geom& g, int Hq, int nsplit);  // what a call with so many splits uses of it
 cudaError_t launch_decode_pages(const Geom& g, PagesArgs a, void* ws, cudaStream_t st);
 
 // page bounds and page selection (kvq_bounds.cu)

@@ -415,7 +415,8 @@ KVQ_API kvq_status kvq_select_pages(const kvq_cache* cache, const void* q, int32
  * rounding, and values by 2^-29 of the largest weight x V scale.  A page copy that does not arrive
  * within the bounded wait flags KVQ_DEV_TIMEOUT.
  * Workspace: kvq_decode_pages_workspace_bytes(), 256-byte aligned, ZERO-FILLED before its first use
- * (its counters are left at zero again).  As with kvq_plan_pages it serves any shapes in turn; two
+ * (its counters are left at zero again): the bytes for this budget and every smaller one.  As with
+ * kvq_plan_pages it serves any shapes in turn; two
  * calls in flight at once on one workspace race.
  */
 KVQ_API size_t kvq_decode_pages_workspace_bytes(const kvq_cache* cache, int32_t num_q_heads, int32_t budget);

@@ -59,3 +59,12 @@ def test_one_workspace_for_plans_selections_and_attention(kvq):
         wt, wcu, slots, pos, ids, left, bits = plan_reference(L, new, table, free, free_n, most)
         assert t["slots"][:most].tolist() == slots and t["pos"][:most].tolist() == pos and t["ids"][:most].tolist() == ids
         assert t["cu"].tolist() == wcu.tolist() and int(t["count"]) == left and c.read_status() == bits == 0
+
+
+def test_the_workspace_of_a_budget_serves_smaller_ones(kvq):
+    cache = filled(kvq, 1, 8, 0, 4, 64, torch.bfloat16, lengths=[130 * G - 7])
+    q = randn(gen(2), 1, 32, D).to(torch.bfloat16)
+    ws = torch.zeros(kvq.kvq_decode_pages_workspace_bytes(cache.c, 32, 128), dtype=torch.uint8, device="cuda")
+    for budget in (128, 72, 73, 96, 5, 1, 110, 16):
+        lists, n = random_lists(cache, budget, budget)
+        within(attend(cache, q, lists, n, ws=ws), *attend_reference(kvq, cache, q, lists, n, D ** -0.5))
