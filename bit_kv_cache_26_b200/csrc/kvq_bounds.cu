@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kSelThreads, 6) select_pages_kernel(Geom g, Se
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-      last = arrive_last(a.counters, grp, a.counter_bits, a.nsplit);
+      last = arrive_last(a.counters, (int)grp, a.counter_sharing, a.nsplit);
     }
     __syncthreads();
     if (!last) return;
@@ -437,10 +437,10 @@ cudaError_t launch_select(const Geom& g, SelectArgs a, void* ws, int num_sms, cu
   const size_t groups = (size_t)g.B * g.H;
   a.minus_zero = -0.0f;
   a.counters = (unsigned*)ws;
-  a.counter_bits = counter_bits((int64_t)groups);
+  a.counter_sharing = counter_sharing((int64_t)groups);
   a.keys = (uint32_t*)((uint8_t*)ws + kCounterBytes);
   // as many CTAs as six per SM, each with 32 pages (one round of its warps) or more
-  const int64_t most = std::min<int64_t>(std::max(1, g.maxp / 32), a.counter_bits ? (INT64_C(1) << a.counter_bits) - 1 : 1);
+  const int64_t most = std::min<int64_t>(std::max(1, g.maxp / 32), most_arrivals(a.counter_sharing));
   a.nsplit = (int)std::min<int64_t>(most, std::max<int64_t>(1, 6 * (int64_t)num_sms / (int64_t)groups));
   const dim3 grid(a.nsplit, g.H, g.B);
   auto* kernel = g.dtype == KVQ_BF16 ? select_pages_kernel<true> : select_pages_kernel<false>;

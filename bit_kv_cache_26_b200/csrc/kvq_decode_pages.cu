@@ -1041,7 +1041,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    last = arrive_last(a.counters, grp, a.counter_bits, a.nsplit);
+    last = arrive_last(a.counters, (int)grp, a.counter_sharing, a.nsplit);
   }
   __syncthreads();
   if (!last) return;
@@ -1144,7 +1144,7 @@ int decode_pages_splits(const Geom& g, int Gq, int budget_, int num_sms) {
   const int by_smem = 233472 / (pages_smem((int)g.sub_bytes, Gq > 8 ? 2 : 1, wide, g.P).total + 1024 + 128);
   const int64_t occ = std::max(1, std::min(by_regs, by_smem));
   // (through the workspace only where the groups' counters hold the splits, which no group count past 256 wants)
-  const int most = (int)std::min<int64_t>(counter_bits(units) >= 8 ? 64 : 8, budget);
+  const int most = (int)std::min<int64_t>(most_arrivals(counter_sharing(units)) >= 64 ? 64 : 8, budget);
   auto round = [&](int64_t k, int64_t pages) { return 5.0 + 1.25 * (k - 1) + pages * std::max(1.0, 0.48 * k); };
   int best = 1;
   double best_cost = 1e300;
@@ -1181,7 +1181,7 @@ cudaError_t launch_decode_pages(const Geom& g0, PagesArgs a, void* ws, cudaStrea
   // 16 splits measured the same either way
   a.clustered = meet_in_clusters(a.nsplit);
   a.counters = (unsigned*)ws;
-  a.counter_bits = counter_bits((int64_t)g.B * g.H);
+  a.counter_sharing = counter_sharing((int64_t)g.B * g.H);
   // the rows of 128 first: they are read 16 bytes at a time, which an odd number of (max, sum) pairs before them would not allow
   a.part_o = (float*)((uint8_t*)ws + kCounterBytes);
   a.part_ml = a.part_o + kD * (size_t)g.B * a.Hq * a.nsplit;

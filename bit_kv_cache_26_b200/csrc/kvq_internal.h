@@ -46,7 +46,7 @@ struct PagesArgs {
   float* part_ml;
   float* part_o;
   unsigned* counters;
-  int counter_bits;
+  int counter_sharing;
 };
 int decode_pages_splits(const Geom& g, int Gq, int budget, int num_sms);
 int decode_pages_most_splits(const Geom& g, int Gq, int budget, int num_sms);  // of all budgets up to this one
@@ -65,7 +65,7 @@ struct SelectArgs {
   int32_t* list_len;
   unsigned* counters;
   uint32_t* keys;
-  int nsplit, counter_bits;
+  int nsplit, counter_sharing;
   float minus_zero;
 };
 size_t select_workspace(const Geom& g);

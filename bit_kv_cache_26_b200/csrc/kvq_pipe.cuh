@@ -42,14 +42,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t phase, uint32_
 }
 
 // The arrival counters of a workspace: its first kCounterBytes, zero between calls.  No call keeps anything else there,
-// whatever the shape, so that one workspace serves calls of different shapes in turn.  A group's counter has `bits` bits of
-// its word: 32 for up to 64 groups, 16, 8 and 4 for up to 128, 256 and 512 (0: more groups have none).
+// whatever the shape, so that one workspace serves calls of different shapes in turn.  1, 2, 4 or 8 groups share a word (2 to
+// the power returned here), for up to 64, 128, 256 and 512 groups; more have no counters (-1).
 constexpr int kCounterBytes = 256;
-inline int counter_bits(int64_t groups) { return groups <= 64 ? 32 : groups <= 128 ? 16 : groups <= 256 ? 8 : groups <= 512 ? 4 : 0; }
-// One arrival of the n < 2^bits of group grp: true for the last, which leaves the counter at zero.
-__device__ __forceinline__ bool arrive_last(unsigned* counters, int64_t grp, int bits, unsigned n) {
-  const int per = 32 / bits, shift = (int)(grp % per) * bits;
-  unsigned* word = counters + grp / per;
+inline int counter_sharing(int64_t groups) { return groups <= 64 ? 0 : groups <= 128 ? 1 : groups <= 256 ? 2 : groups <= 512 ? 3 : -1; }
+inline int64_t most_arrivals(int sharing) { return sharing < 0 ? 1 : (INT64_C(1) << (32 >> sharing)) - 1; }
+// One arrival of the n <= most_arrivals of group grp: true for the last, which leaves the counter at zero.
+__device__ __forceinline__ bool arrive_last(unsigned* counters, int grp, int sharing, unsigned n) {
+  const int bits = 32 >> sharing, shift = (grp & ((1 << sharing) - 1)) * bits;
+  unsigned* word = counters + (grp >> sharing);
   const bool last = (atomicAdd(word, 1u << shift) >> shift & (0xffffffffu >> (32 - bits))) == n - 1u;
   if (last) atomicSub(word, n << shift);
   return last;
