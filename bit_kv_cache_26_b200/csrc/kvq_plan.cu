@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_once_kernel(Geom g, PlanArg
         before[b] = (int32_t)at.y;
         end = next;
         ++n_mine;
-      } else if (mine[i].x > 0 && blockIdx.x == 0) {
+      } else if (at.x <= a.max_tokens && at.y <= free_n && blockIdx.x == 0) {  // the first that does not fit
         set_status(g.status, next.y > free_n ? KVQ_DEV_NO_PAGES : KVQ_DEV_OVERFLOW);
       }
       at = next;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kPlanScan) plan_scan_kernel(Geom g, PlanArgs a
     if (served) {
       a.cu[b + 1] = (int32_t)upto.x;
       a.ws[kPlanData + 2 + b] = (int32_t)(upto.y - mine.y);
-    } else if (mine.x > 0) {
+    } else if (b < g.B && upto.x - mine.x <= a.max_tokens && upto.y - mine.y <= free_n) {  // the first that does not fit
       set_status(g.status, upto.y > free_n ? KVQ_DEV_NO_PAGES : KVQ_DEV_OVERFLOW);
     }
     carry = add2ll(carry, warp_tot[nw - 1]);
