@@ -55,10 +55,18 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int i, int lo, int hi) 
   return lo;
 }
 
+// Slot of position pos in page phys; an invalid page id, from the table or the stack, has none (-1) and is noted in `bad`.
+__device__ __forceinline__ int64_t slot_of(const Geom& g, int phys, int pos, bool& bad) {
+  const bool ok = (unsigned)phys < (unsigned)g.npages;
+  bad = bad || !ok;
+  return ok ? (int64_t)phys * kG + pos % kG : -1;
+}
+
 // Packed tokens [begin, end) of the plan, two consecutive ones per thread and round (a warp's stores are whole sectors).  cu, before (new pages of the
 // sequences before) and len: in shared or global memory.
 __device__ __forceinline__ void expand(const Geom& g, const PlanArgs& a, const int32_t* cu, const int32_t* before,
                                        const int32_t* len, int begin, int end, int s_lo, int s_hi, int free_n) {
+  bool bad = false;
   if (s_lo == s_hi && end - begin == 2 * kPlanThreads * kPlanAhead) {
     // the whole chunk in one sequence, as in a long prompt: the page ids of all rounds first, then the stores
     const int s = s_lo, L = len[s], held = (L + kG - 1) / kG, top = free_n - 1 - (before[s] - held);
@@ -80,11 +88,11 @@ __device__ __forceinline__ void expand(const Geom& g, const PlanArgs& a, const i
       const int pos = pos0 + 2 * kPlanThreads * u, i0 = begin + 2 * (int)threadIdx.x + 2 * kPlanThreads * u;
       *reinterpret_cast<int2*>(a.positions + i0) = make_int2(pos, pos + 1);
       *reinterpret_cast<int2*>(a.seq_ids + i0) = make_int2(s, s);
-      *reinterpret_cast<longlong2*>(a.slot_map + i0) =
-          make_longlong2((int64_t)id0[u] * kG + pos % kG, (int64_t)id1[u] * kG + (pos + 1) % kG);
+      *reinterpret_cast<longlong2*>(a.slot_map + i0) = make_longlong2(slot_of(g, id0[u], pos, bad), slot_of(g, id1[u], pos + 1, bad));
       if (pos % kG == 0) row[pos / kG] = id0[u];
       if ((pos + 1) % kG == 0) row[(pos + 1) / kG] = id1[u];
     }
+    if (bad) set_status(g.status, KVQ_DEV_BAD_PAGE);
     return;
   }
   for (int i0 = begin + 2 * (int)threadIdx.x; i0 < end; i0 += 2 * kPlanThreads) {
@@ -110,7 +118,7 @@ __device__ __forceinline__ void expand(const Geom& g, const PlanArgs& a, const i
           page = p;
           phys = p < held ? g.page_table[(int64_t)s * g.maxp + p] : a.free_pages[free_n - 1 - (before[s] + p - held)];
         }
-        slot[e] = (int64_t)phys * kG + pos[e] % kG;
+        slot[e] = slot_of(g, phys, pos[e], bad);
         if (pos[e] % kG == 0) const_cast<int32_t*>(g.page_table)[(int64_t)s * g.maxp + p] = phys;
       }
     }
@@ -124,6 +132,7 @@ __device__ __forceinline__ void expand(const Geom& g, const PlanArgs& a, const i
       a.slot_map[i0] = slot[0];
     }
   }
+  if (bad) set_status(g.status, KVQ_DEV_BAD_PAGE);
 }
 
 // One launch: every CTA scans all requests (consecutive ones per thread) into shared memory and writes its chunk of

@@ -355,6 +355,8 @@ KVQ_API kvq_status kvq_norm_rope(const kvq_rows* q, const kvq_rows* k, const kvq
  * A request with a negative length or past the page table flags KVQ_DEV_OVERFLOW and gets nothing.
  * When the tokens would pass max_tokens (KVQ_DEV_OVERFLOW) or the pages the stack
  * (KVQ_DEV_NO_PAGES, also where both would), that sequence and all after it get nothing.
+ * A token whose page, held or off the stack, has an id outside [0, num_pages) gets slot -1 (KVQ_DEV_BAD_PAGE);
+ * the table takes the stack's id as it is, and the calls that read it pass it over.
  * slot_map, positions and seq_ids are 16-byte aligned.
  * Workspace: kvq_plan_workspace_bytes(), 4-byte aligned, ZERO-FILLED before its first use (its counters are left at
  * zero again).  One workspace, zeroed once, serves calls of any shapes in turn that it is large enough for, and
