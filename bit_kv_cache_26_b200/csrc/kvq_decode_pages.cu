@@ -221,6 +221,9 @@ __device__ __forceinline__ float4 peer_f4(const void* p, int r) {
 // 0; a query of NaN has no maximum (it is ignored) and a sum of NaN, which is left to show in the output.
 __device__ __forceinline__ float sum_or_one(float l) { return l == 0.f ? 1.f : l; }
 
+// Whether v is a finite number of the output's type (fp16 rounds to infinity from 65520 on).
+__device__ __forceinline__ bool in_range(const Geom& g, float v) { return fabsf(v) < (g.dtype == KVQ_BF16 ? INFINITY : 65520.0f); }
+
 // Output of one query head from its channels 4 lane .. 4 lane + 3 of sum p v and its sum p.
 __device__ __forceinline__ void finish_head(const Geom& g, float (&o)[4], float l, const float* vcol, uint16_t* out, int lane) {
   const float inv = 1.0f / l;
@@ -242,7 +245,7 @@ __device__ __forceinline__ void finish_head(const Geom& g, float (&o)[4], float 
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[k] *= 0.0078125f;
   }
-  if (!(isfinite(o[0]) && isfinite(o[1]) && isfinite(o[2]) && isfinite(o[3]))) set_status(g.status, KVQ_DEV_RANGE);
+  if (!(in_range(g, o[0]) && in_range(g, o[1]) && in_range(g, o[2]) && in_range(g, o[3]))) set_status(g.status, KVQ_DEV_RANGE);
   uint2 r;
   if (g.dtype == KVQ_BF16) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(o[0], o[1]), y = __floats2bfloat162_rn(o[2], o[3]);
@@ -984,7 +987,7 @@ __global__ void __launch_bounds__(kNW * 32, WIDE ? (NT == 1 ? 3 : 2) : 4) decode
         for (int i = 0; i < NH; ++i) {
           if (i < Gq) {
             const float v = o[i] * sum_ml[i].x;
-            bad = bad || !isfinite(v);
+            bad = bad || !in_range(g, v);
             a.out[((int64_t)b * a.Hq + (int64_t)h * Gq + i) * kD + c] =
                 g.dtype == KVQ_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
           }

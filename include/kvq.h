@@ -132,7 +132,8 @@ typedef enum {
 #define KVQ_DEV_OVERFLOW 0x2   /* seq_len + n_new > max_pages_per_seq * 32 */
 #define KVQ_DEV_BAD_SET 0x4    /* seq_to_set entry outside [0, num_sets) */
 #define KVQ_DEV_TIMEOUT 0x8    /* a bounded wait for a page copy expired; that step's output is invalid */
-#define KVQ_DEV_RANGE 0x10     /* decode: |q_d * s_d| or a V scale exceeded the fp16 operand range (~3e4) */
+#define KVQ_DEV_RANGE 0x10     /* decode: an output is not finite in its type: a scale past the operand range, a value past the
+                                  type's, or an infinity or NaN among the inputs */
 #define KVQ_DEV_NO_PAGES 0x20  /* kvq_plan_pages: the free list ran out; the sequences after that got no tokens */
 
 typedef enum { KVQ_F16 = 0, KVQ_BF16 = 1 } kvq_dtype;
@@ -411,7 +412,7 @@ KVQ_API kvq_status kvq_select_pages(const kvq_cache* cache, const void* q, int32
  *   (KVQ_DEV_BAD_PAGE); a list_len outside 0..budget counts as 0 (KVQ_DEV_OVERFLOW).
  *   q, out [num_seqs][num_q_heads][128] dtype: unlike kvq_decode_attention's, `out` is in the
  *   cache's dtype (softmax and sums in fp32, rounded once).  No entries: zeros.
- * NaN in a query shows in its head's output.  The same inputs give the same bits on every run.
+ * NaN in a query shows in its head's output (KVQ_DEV_RANGE, as of any output that is not finite in its type).  The same inputs give the same bits on every run.
  * K scales above about 2000 leave the operands' range (KVQ_DEV_RANGE); logits are off by at most
  * 2^-17 sm_scale max |q_d| (of the transformed query under the pre-transform) beside fp32's own
  * rounding, and values by 2^-29 of the largest weight x V scale.  A page copy that does not arrive

@@ -97,3 +97,28 @@ def test_pages_of_very_different_values(kvq):
         sub[at + 1056:at + 1088] = 255                               # without patterns
     for order in ([0, 1, 2, 3, 4, 5], [3, 1, 0], [1, 4], [4], [1, 0], [5, 4, 3, 2, 1, 0]):
         check(kvq, cache, q, order)
+
+
+@pytest.mark.parametrize("tx", [0, 1])
+@pytest.mark.parametrize("pages", [1, 8, 64])                        # one CTA, a cluster, splits that meet in the workspace
+def test_outputs_past_the_type_are_flagged(kvq, pages, tx):
+    cache, q = sink_cache(kvq, torch.float16, 4, 4, pages, 0, 0, 1.0, tx)
+    order = list(range(pages))
+    at = 2 * (G * D * 4 // 8) + 1024
+    for b in range(pages):                                           # values of 1 where they were, without patterns and transform
+        sub = cache.subblock(0, b, 0)
+        f = sub[at:at + 1024].view(torch.float32)
+        f[:128], f[128:] = 0.0, 1.0
+        sub[at + 1056:at + 1088] = 255
+        if tx:
+            sub[at + 1088 + 128:at + 1088 + 256].view(torch.float32).fill_(1.0)
+    lists = torch.tensor(order, dtype=torch.int32, device="cuda").view(1, 1, -1)
+    n = torch.full((1, 1), pages, dtype=torch.int32, device="cuda")
+    base = attend(cache, q, lists, n).float().abs().max()            # (under the transform, one channel of its own size)
+    assert cache.read_status() == 0
+    for want, flagged in ((65500.0, False), (65600.0, True), (1e6, True)):
+        for b in range(pages):
+            cache.subblock(0, b, 0)[at + 512:at + 1024].view(torch.float32).fill_(want / float(base))
+        out = attend(cache, q, lists, n)
+        assert bool(torch.isinf(out).any()) == flagged
+        assert cache.read_status(clear=True) == (kvq.KVQ_DEV_RANGE if flagged else 0)
