@@ -359,8 +359,13 @@ __device__ void take_largest(const uint32_t* keys, int m, int k, int base, int32
   }
 }
 
+// CTAs an SM holds: by shared memory (228 KB, of which each takes 1 KB besides its own).
+constexpr int kSelCtas = 5;
+constexpr int kSelSmem = kSelRing + 2 * kD * 4 + (int)sizeof(Chooser) + 4 * kLocalKeys + 16 + 1024;
+static_assert(kSelCtas * kSelSmem <= 228 * 1024 && (kSelCtas + 1) * kSelSmem > 228 * 1024, "the CTAs an SM holds");
+
 template <bool BF16>
-__global__ void __launch_bounds__(kSelThreads, 6) select_pages_kernel(Geom g, SelectArgs a) {
+__global__ void __launch_bounds__(kSelThreads, kSelCtas) select_pages_kernel(Geom g, SelectArgs a) {
   __shared__ float W[2 * kD];
   __shared__ Chooser chooser;
   __shared__ uint32_t local_keys[kLocalKeys];
@@ -439,9 +444,9 @@ cudaError_t launch_select(const Geom& g, SelectArgs a, void* ws, int num_sms, cu
   a.counters = (unsigned*)ws;
   a.counter_sharing = counter_sharing((int64_t)groups);
   a.keys = (uint32_t*)((uint8_t*)ws + kCounterBytes);
-  // as many CTAs as six per SM, each with 32 pages (one round of its warps) or more
+  // as many CTAs as the SMs hold at once, each with 32 pages (one round of its warps) or more
   const int64_t most = std::min<int64_t>(std::max(1, g.maxp / 32), most_arrivals(a.counter_sharing));
-  a.nsplit = (int)std::min<int64_t>(most, std::max<int64_t>(1, 6 * (int64_t)num_sms / (int64_t)groups));
+  a.nsplit = (int)std::min<int64_t>(most, std::max<int64_t>(1, kSelCtas * (int64_t)num_sms / (int64_t)groups));
   const dim3 grid(a.nsplit, g.H, g.B);
   auto* kernel = g.dtype == KVQ_BF16 ? select_pages_kernel<true> : select_pages_kernel<false>;
   // the kernel's shared-memory limit is raised once per device
