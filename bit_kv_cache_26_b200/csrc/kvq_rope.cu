@@ -165,9 +165,12 @@ cudaError_t launch_norm_rope(const RopeArgs& a0, int dtype, bool interleaved, in
   const int64_t groups = (a.rows[0].heads + 3) / 4 + (a.rows[1].heads + 3) / 4 + (a.rows[2].heads + 3) / 4;
   const int64_t warps = (int64_t)num_sms * 32;
   a.parts = (int)std::min(groups, std::max<int64_t>(1, warps / a.tokens));
-  // One to three waves of warps: halves even out the last one, where the angles made twice are little beside the rows (12
-  // groups a token, 5000, 10000 and 20000 tokens: 32, 51 and 90 us whole, 28, 49 and 90 in halves; 9 groups, 8191 tokens: 31, 33).
-  if (a.parts == 1 && groups >= 10 && a.tokens < 3 * warps) a.parts = 2;
+  // One to three waves of warps, the last less than half full: halves even it out, where the angles made twice are little
+  // beside the rows.  12 groups a token (4736 tokens a wave), whole and in halves: 4800 tokens 31 and 28 us, 6500 35 and 32,
+  // 9600 49 and 47; with the last wave fuller, 7300 37 and 38, 12000 55 and 56; past three waves no better (16000: 72 and 72).
+  // 6 groups: 4800 tokens 17.6 and 16.0 us, 6900 20.4 and 19.9, 8191 22 and 23; 3 groups: slower everywhere.
+  if (a.parts == 1 && groups >= 6 && a.tokens < 3 * warps && a.tokens % warps > 0 && 2 * (a.tokens % warps) < warps && a.tokens > warps)
+    a.parts = 2;
   const int64_t grid = (a.tokens * a.parts + kRopeWarps - 1) / kRopeWarps;
   const bool bf = dtype == KVQ_BF16;
   auto* k = bf ? (interleaved ? norm_rope_kernel<true, true> : norm_rope_kernel<true, false>)
