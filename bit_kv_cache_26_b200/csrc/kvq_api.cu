@@ -40,6 +40,19 @@ int num_sms() {
   return sms;
 }
 
+// Whether two of the n x m rows of 128 elements at i * si + j * sj share an element.
+bool rows_overlap(int64_t n, int64_t si, int64_t m, int64_t sj) {
+  if ((n > 1 && si < 128) || (m > 1 && sj < 128)) return true;
+  if (n == 1 || m == 1) return false;
+  if (si >= 128 && (si - 128) / sj >= m - 1) return false;  // all of one dimension within a step of the other, as usual
+  if (sj >= 128 && (sj - 128) / si >= n - 1) return false;
+  for (int64_t j = 1; j < m; ++j) {  // the multiples of si on both sides of j * sj
+    const int64_t i = j * (sj / si) + j * (sj % si) / si, over = j * (sj % si) % si;
+    if ((i < n && over < 128) || (i + 1 < n && si - over < 128)) return true;
+  }
+  return false;
+}
+
 kvq_status check_cache(const kvq_cache* c) {
   if (!c) return fail(KVQ_ERR_INVALID_ARG, "cache is NULL");
   if (c->head_dim != 128) return fail(KVQ_ERR_UNSUPPORTED, "head_dim %d unsupported (only 128)", c->head_dim);
@@ -269,15 +282,15 @@ kvq_status kvq_norm_rope(const kvq_rows* q, const kvq_rows* k, const kvq_rows* v
     if (r->in_tok_stride % 8 || r->in_head_stride % 8 || r->out_tok_stride % 8 || r->out_head_stride % 8 ||
         r->in_tok_stride < 0 || r->in_head_stride < 0 || r->out_tok_stride < 0 || r->out_head_stride < 0)
       return fail(KVQ_ERR_INVALID_ARG, "strides must be multiples of 8 elements, not negative");
-    if ((r->heads > 1 && r->out_head_stride < 128) || (num_tokens > 1 && r->out_tok_stride < 128))
-      return fail(KVQ_ERR_INVALID_ARG, "output rows overlap (strides %lld, %lld)", (long long)r->out_tok_stride,
-                  (long long)r->out_head_stride);
     if (i == 2 && r->weight) return fail(KVQ_ERR_INVALID_ARG, "values take no weight");
     a.rows[i] = {r->in, r->out, r->weight, r->heads, r->in_tok_stride, r->in_head_stride, r->out_tok_stride,
                  r->out_head_stride};
   }
   if (num_tokens == 0 || heads == 0) return KVQ_OK;
   if (heads > 65535) return fail(KVQ_ERR_CAPACITY, "%lld heads in all exceed 65535", (long long)heads);
+  for (const kvq::RopeRows& r : a.rows)
+    if (r.heads > 0 && rows_overlap(num_tokens, r.out_tok, r.heads, r.out_head))
+      return fail(KVQ_ERR_INVALID_ARG, "output rows overlap (strides %lld, %lld)", (long long)r.out_tok, (long long)r.out_head);
   const bool turned = a.rows[0].heads + a.rows[1].heads > 0 && rot_dim > 0;
   if (turned && (!positions || !inv_freq)) return fail(KVQ_ERR_INVALID_ARG, "positions / inv_freq is NULL");
   a.pos = positions;
