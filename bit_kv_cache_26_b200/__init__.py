@@ -210,7 +210,6 @@ def kvq_decode_step(cache: kvq_cache, k_new: torch.Tensor, v_new: torch.Tensor, 
 # ---------------------------------------------------------------------------
 
 _TORCH_DT = {KVQ_F16: torch.float16, KVQ_BF16: torch.bfloat16}
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _want(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int) -> int:
@@ -225,8 +224,8 @@ def _here(stream) -> tuple[int, int]:
     """The current device and the stream to use (the current one unless given)."""
     if not torch.cuda.is_initialized():  # no tensor can be on a device then: the checks that follow say so
         return 0, 0
-    dev = torch._C._cuda_getDevice()
-    return dev, _raw_stream(dev) if stream is None else stream.cuda_stream
+    dev = torch.cuda.current_device()
+    return dev, torch.accelerator.current_stream(dev).native_handle if stream is None else stream.cuda_stream
 
 
 def _ws(ws: torch.Tensor | None, dev: int) -> tuple[int | None, int]:
