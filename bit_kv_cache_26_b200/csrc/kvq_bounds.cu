@@ -15,9 +15,9 @@
 //   term_d = fl(fl(W+_d hi_d) + fl(W-_d lo_d)); 8 neighbouring channels halved (4, 2, 1), then
 //   the 16 sums halved (8, 4, 2, 1).  Equal scores: the lower page.  NaN ranks above all.
 //
-// Bound: HBM.  One B200: bounds of 8 x 32768 keys x 8 heads 94 us (6.1 TB/s, 0.93 of the copy
-// bandwidth); selection over 256 sequences x 8 heads x 512 pages 100 us (5.4 TB/s, 0.82), for one
-// sequence of 1024 pages 10.5 us of latency (lengths, page ids, bounds, the last CTA's choice).  The
+// Bound: HBM.  One B200: bounds of 8 x 32768 keys x 8 heads 93 us (6.1 TB/s, 0.93 of the copy
+// bandwidth); selection over 256 sequences x 8 heads x 512 pages 98 us (5.5 TB/s, 0.84), for one
+// sequence of 1024 pages 10.6 us of latency (lengths, page ids, bounds, the last CTA's choice).  The
 // query heads are loaded before the first is used: 16 heads a group in turn took 12.8 us for 9.2 there.
 #include <algorithm>
 #include <atomic>

@@ -3,15 +3,15 @@
 // ("PatternKV", Section 3.4: the fused reconstruction and attention, over a subset of the pages).
 //
 // Bound: the listed sub-blocks from HBM, then instruction issue.  One B200, 256 sequences x 8 KV heads
-// x 128 of 512 pages in 4 bits, 4 query heads each: 308-317 us, 5.2-5.3 TB/s of page bytes (0.78-0.81 of
-// the copy bandwidth); 361 us back to back, under the power cap.  With 8 and 16 heads a group (1024
-// groups of 64 pages) 135 and 264 us for 63 of bytes: the work per page grows with the heads, and 12 and
-// 8 warps an SM hide less of it.  The setup and merge of a CTA (lengths, ids, q . M_K, W . M_V) are a
-// tenth of the first and most of the time of short lists: they avoid branches and loads that wait for
-// each other (all query rows at once, four heads' sums exchanged together, the final sum eight patterns
-// at a time), which took 55 us for 78 at 912 groups of 3 pages with 5 query heads and 106 patterns.  The
-// first form, with pattern weights added by lanes in turn and both lanes of a head forming every
-// product, took 481 us in the first case; scalar instead of packed pairs in the loop 324.
+// x 128 of 512 pages in 4 bits, 4 query heads each: 338-346 us, 4.7-4.8 TB/s of page bytes (0.72-0.74 of
+// the copy bandwidth); 386 us back to back, under the power cap; in 2 bits, of two thirds of the bytes, 328
+// us (nearly the same instructions).  With 8 and 16 heads a group (1024 groups of 64 pages) 176 and 347 us
+// for 63 of bytes: the work per page grows with the heads, and 12 and 8 warps an SM hide less of it.  The
+// setup and merge of a CTA (lengths, ids, q . M_K, W . M_V) are a tenth of the first and most of the time
+// of short lists: they avoid branches and loads that wait for each other (all query rows at once, four
+// heads' sums exchanged together, the final sum eight patterns at a time).  Two choices cost time for
+// what they keep: pattern weights as fp32 sums in a fixed order took 308 -> 334 us (of which finding the
+// tokens that share a pattern 13), V operands in units that follow their size 334 -> 338.
 //
 // Per CTA one (sequence, KV head, split of the list); each warp streams its entries' sub-blocks
 // through a ring of shared-memory stages (cp.async.bulk, bounded mbarrier waits).
@@ -28,10 +28,10 @@
 // row factor (undone on the sums) and a column factor (folded into B).  B is q s or p s in fp16
 // hi + lo parts (22 bits).  The query is scaled by a power of two to [16, 32): K scales up to 2000 fit
 // fp16 (past them the output is not finite and KVQ_DEV_RANGE is set); of a product too small for hi + lo
-// 2^-25 is dropped, as if the key's scale were off by 2^-29 (2^-25 in columns with a factor).  p s is in units that follow the largest
-// product a head has met in the warp (below 2^15 of them), so that a dominant token of small value, or
-// values that are small throughout, leave the others their bits: what is dropped is 2^-33 of that
-// product (2^-29 where columns have a factor).
+// 2^-25 is dropped, as if the key's scale were off by 2^-29 (2^-25 in columns with a factor).  p s is in
+// units that follow the largest product a head has met in the warp (below 2^15 of them), so that a dominant
+// token of small value, or values that are small throughout, leave the others their bits: what is dropped
+// is 2^-33 of that product (2^-29 where columns have a factor).
 //
 // Up to four query heads per KV head: the eight columns of a product are (head, {hi, lo}).  The two
 // lanes of a head's columns each form the products of half the channels (tokens for V) and give each
@@ -1129,9 +1129,10 @@ cudaError_t launch_bits(const Geom& g, const PagesArgs& a, cudaStream_t st) {
 // Model, in units of the time a lone CTA takes for a page per warp (1.3 us on one B200): k CTAs on an SM at once take
 // max(1, 0.48 k) for a page per warp and 5 + 1.25 (k - 1) before and after the loop; the busiest SM runs its CTAs `occ` at a
 // time; merging costs a little per split, and more per head through the workspace (8 groups of 64 pages, 8 splits and 16:
-// 11.3 and 11.2 us with 4 heads a group, 13.8 and 14.8 with 8, 18.4 and 22.0 with 16).  Measured with 4, 8 and 16 heads a group at 64 listed pages for 8 groups (best 8 splits; 1: 27, 39 and 60 us; 64:
-// 18, 35 and 53), 128 groups (2) and 1024 (1), at 256 pages for 16 (16), at 128 pages for 256 (1; with 4 heads 2 are a
-// twentieth faster), at 452 pages for 3 (33): the model's choice or within a tenth of it.
+// 10.7 and 10.4 us with 4 heads a group, 13.4 and 14.4 with 8, 18.6 and 21.2 with 16).  Measured best with 4, 8 and 16 heads a
+// group at 64 listed pages: for 8 groups 16, 8 and 8 splits (1: 30, 41 and 67 us; 64: 17, 34 and 52), for 64 groups 4, for 128
+// groups 2, for 1024 groups 1; at 256 pages for 16 groups 16 (8: 23, 32 and 52 us for 17.5, 24 and 39); at 128 pages for 256
+// groups 1 (with 4 heads 2: 62 us for 68); at 452 pages for 3 groups 47.  The model's choice is the best or within a tenth of it.
 // The budget is rounded up to eight sizes per power of two first, so that the largest choice of all budgets up to one is
 // found by trying few.
 static int64_t rounded_budget(int64_t budget) {
@@ -1154,7 +1155,7 @@ int decode_pages_splits(const Geom& g, int Gq, int budget_, int num_sms) {
   for (int ns = 1; ns <= most; ns = ns < 16 ? 2 * ns : ns + ns / 8) {
     const int64_t per_sm = (units * ns + sms - 1) / sms, full = per_sm / occ, rem = per_sm % occ;
     const int64_t pages = ((budget + ns - 1) / ns + kNW - 1) / kNW;
-    const double cost = full * round(occ, pages) + (rem ? round(rem, pages) : 0.0) + 0.05 * ns + (ns >= 16 ? 0.2 * Gq : 0.0);
+    const double cost = full * round(occ, pages) + (rem ? round(rem, pages) : 0.0) + 0.05 * ns + (ns >= 16 ? 0.1 * Gq : 0.0);
     if (cost < best_cost * (1.0 - 1e-9)) { best_cost = cost; best = ns; }
   }
   return best;
@@ -1180,8 +1181,7 @@ size_t decode_pages_need(const Geom& g, int Hq, int nsplit) {
 cudaError_t launch_decode_pages(const Geom& g0, PagesArgs a, void* ws, cudaStream_t st) {
   Geom g = g0;
   g.wait_limit = page_wait_limit(g0.wait_limit);
-  // 64 groups of 64 pages, 4 splits: 17.1 us as clusters, 20.8 us through the workspace; 8 groups, 8 splits: 11.1 / 13.6 us;
-  // 16 splits measured the same either way
+  // 64 groups of 64 pages, 4 splits: 16.9 us as clusters, 18.0 us through the workspace; 8 groups, 8 splits: 10.7 / 11.6 us
   a.clustered = meet_in_clusters(a.nsplit);
   a.counters = (unsigned*)ws;
   a.counter_sharing = counter_sharing((int64_t)g.B * g.H);

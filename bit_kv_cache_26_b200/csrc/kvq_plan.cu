@@ -6,9 +6,10 @@
 // A sequence is served when the scans up to and including it stay within the slot map and the
 // stack; both scans only grow, so the served ones are those before the first that does not fit.
 //
-// Bound: latency for a decode step (256 sequences of one token: 4.5 us on one B200), 16 bytes written
-// per token for prompts (256 of up to 16384 tokens, 3.1 M in all: 15.6 us, 3.3 TB/s; every CTA's scan
-// before its first store is a fifth of it).  Two launches, the scan and the expansion, took 17 us there
+// Bound: latency for a decode step (256 sequences of one token: 4.6-5.0 us on one B200); for prompts 16 bytes
+// written per token, after latency (256 of up to 16384 tokens, 51 MB in all: 16.0-16.4 us, 3.2 TB/s, half of the
+// copy bandwidth): every CTA scans the requests before its first store and starts each chunk of 1024 tokens with
+// two barriers, a search and the loads of its page ids.  Two launches, the scan and the expansion, took 17 us there
 // and 7.2 us for the decode step.
 #include <algorithm>
 
