@@ -351,6 +351,8 @@ KVQ_API kvq_status kvq_norm_rope(const kvq_rows* q, const kvq_rows* k, const kvq
  *   cu_new [num_seqs + 1]   first packed token of each sequence, then the total
  *   slot_map [max_tokens]   int64 page id * 32 + slot of each packed token
  *   positions, seq_ids [max_tokens]  int32 position in, and index of, its sequence
+ * (kvq_page_bounds and kvq_quantize_append take one n_new for all sequences of their cache: sequences
+ * that got different numbers of tokens are appended by calls on caches of those alike.)
  * Entries past the total keep what they held.  free_pages [free_capacity] ids, *free_count of them
  * free (device); *free_left = what remains (may be free_count itself: the stack is then popped).
  * A request with a negative length or past the page table flags KVQ_DEV_OVERFLOW and gets nothing.
@@ -415,8 +417,8 @@ KVQ_API kvq_status kvq_select_pages(const kvq_cache* cache, const void* q, int32
  * NaN in a query shows in its head's output (KVQ_DEV_RANGE, as of any output that is not finite in its type).  The same inputs give the same bits on every run.
  * K scales above about 2000 leave the operands' range (KVQ_DEV_RANGE); logits are off by at most
  * 2^-17 sm_scale max |q_d| (of the transformed query under the pre-transform) beside fp32's own
- * rounding, and values by 2^-29 of the largest weight x V scale.  A page copy that does not arrive
- * within the bounded wait flags KVQ_DEV_TIMEOUT.
+ * rounding, and what a token adds to a value by its code x 2^-29 of the largest weight x V scale met.
+ * A page copy that does not arrive within the bounded wait flags KVQ_DEV_TIMEOUT.
  * Workspace: kvq_decode_pages_workspace_bytes(), 256-byte aligned, ZERO-FILLED before its first use
  * (its counters are left at zero again): the bytes for this budget and every smaller one.  As with
  * kvq_plan_pages it serves any shapes in turn; two
